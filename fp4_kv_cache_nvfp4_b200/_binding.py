@@ -79,6 +79,14 @@ def lib() -> ctypes.CDLL:
             L.csa2_attn_lse_merge.argtypes = [_I32, _P, _P, _P, _P, _I32, _P]
             for n in ("csa2_indexer_score_ids", "csa2_topk_merge", "csa2_attn_lse_merge"):
                 getattr(L, n).restype = _I32
+            L.csa2_dense_attn_workspace_bytes.argtypes = [ctypes.POINTER(LayerDesc), _I32, _I32]
+            L.csa2_dense_attn_workspace_bytes.restype = _SZ
+            L.csa2_dense_attn_decode.argtypes = [ctypes.POINTER(LayerDesc), ctypes.POINTER(_Cache), _P, _P, _P, _I32,
+                                                 _P, _I32, _I64, _P, _SZ, _P, _P]
+            L.csa2_dense_attn_prefill.argtypes = [ctypes.POINTER(LayerDesc), ctypes.POINTER(_Cache), _P, _P, _P, _P,
+                                                  _P, _I32, _P, _I32, _I32, _I64, _P, _SZ, _P, _P]
+            for n in ("csa2_dense_attn_decode", "csa2_dense_attn_prefill"):
+                getattr(L, n).restype = _I32
             L.csa2_swa_replay.argtypes = [_P, _P, _P, _P, _I32, _I32, _I32, _P, _P]
             L.csa2_swa_replay.restype = _I32
             L.csa2_test_empty_chain.argtypes = [_I32, _I32, _I32, _P, _P]
@@ -108,6 +116,32 @@ def _stream(stream) -> int | None:
 def _check(status: int, what: str) -> None:
     if status != 0:
         raise CSA2Error(status, what)
+
+
+_BITS16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _tensor(name: str, t, dtypes, shape, optional: bool = False) -> None:
+    """Raise unless t is a contiguous tensor of one of the dtypes and of that
+    shape (None: any size).  What is on a GPU has to be on the current one."""
+    if t is None and optional:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if len(t.shape) != len(shape) or any(w is not None and w != g for g, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous (strides {t.stride()})")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _on_gpu(name: str, t, dtypes, shape, optional: bool = False) -> None:
+    _tensor(name, t, dtypes, shape, optional)
+    if t is not None and not t.is_cuda:
+        raise ValueError(f"{name}: on {t.device}, expected the GPU")
 
 
 def abi_version() -> int:
@@ -201,6 +235,29 @@ class KVCache:
                          self.pooled.data_ptr() if pooled else None, self.page_table.data_ptr(), page_size,
                          self.page_table.shape[1], n_phys_pages)
 
+    @classmethod
+    def from_tensors(cls, codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, page_size: int,
+                     idx_k: torch.Tensor | None = None, pooled: torch.Tensor | None = None) -> "KVCache":
+        """A handle on arrays the caller keeps (nothing is copied; the page table
+        may be rewritten in place): codes [n_slots, 128] and scales [n_slots, 16]
+        uint8, page_table int32 [n_seqs, max_pages], idx_k [n_slots, 64] and
+        pooled [n_slots / 8, 64] 16-bit.  Without idx_k and pooled the handle
+        serves the attention calls only."""
+        n = codes.shape[0]
+        if page_size < 1 or n % page_size:
+            raise ValueError(f"{n} slots are not whole pages of {page_size}")
+        _tensor("codes", codes, (torch.uint8,), (n, 128))
+        _tensor("scales", scales, (torch.uint8,), (n, 16))
+        _tensor("page_table", page_table, (torch.int32,), (None, None))
+        _tensor("idx_k", idx_k, _BITS16, (n, 64), optional=True)
+        _tensor("pooled", pooled, _BITS16, (n // 8, 64), optional=True)
+        v = cls.__new__(cls)
+        v.page_size, v.n_phys_pages = page_size, n // page_size
+        v.codes, v.scales, v.idx_k, v.pooled, v.page_table = codes, scales, idx_k, pooled, page_table
+        v._s = _Cache(codes.data_ptr(), scales.data_ptr(), _ptr(idx_k), _ptr(pooled), page_table.data_ptr(),
+                      page_size, page_table.shape[1], v.n_phys_pages)
+        return v
+
     def struct(self) -> _Cache:
         return self._s
 
@@ -250,6 +307,56 @@ def sparse_attn_prefill(desc: LayerDesc, cache: KVCache, q, topk_idx, q_pos, swa
     _check(lib().csa2_sparse_attn_prefill(ctypes.byref(desc), ctypes.byref(cache.struct()), _ptr(q), _ptr(topk_idx),
                                           _ptr(q_pos), _ptr(swa_kv), swa_start, seq_len, _ptr(out), _ptr(lse), T,
                                           _ptr(err), _stream(stream)), "sparse_attn_prefill")
+
+
+_OUT = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def dense_attn_workspace_bytes(desc: LayerDesc, B: int, prefill: bool = False) -> int:
+    return int(lib().csa2_dense_attn_workspace_bytes(ctypes.byref(desc), B, 1 if prefill else 0))
+
+
+def _dense_checks(q, seq_lens, out, lse, workspace, err, B: int) -> int:
+    T = q.shape[0]
+    _on_gpu("q", q, _BITS16, (T, 16, 128))
+    _on_gpu("seq_lens", seq_lens, (torch.int32,), (B,))
+    _on_gpu("out", out, tuple(_OUT), (T, 16, 128))
+    _on_gpu("lse", lse, (torch.float32,), (T, 16))
+    _on_gpu("workspace", workspace, (torch.uint8,), (None,))
+    _on_gpu("err", err, (torch.int32,), (1,), optional=True)
+    return _OUT[out.dtype]
+
+
+def dense_attn_decode(desc: LayerDesc, cache: KVCache, q, seq_lens, out, lse, max_len: int, workspace: torch.Tensor,
+                      err=None, stream=None) -> None:
+    """One token per sequence (q [B, 16, 128] bf16) over every entry of its
+    sequence; out fp32 or bf16, lse fp32 [B, 16]."""
+    B = seq_lens.numel()
+    dt = _dense_checks(q, seq_lens, out, lse, workspace, err, B)
+    if q.shape[0] != B:
+        raise ValueError(f"q: {q.shape[0]} rows for {B} sequences")
+    if cache.page_table.shape[0] < B:
+        raise ValueError(f"seq_lens: {B} sequences, the page table has {cache.page_table.shape[0]}")
+    _check(lib().csa2_dense_attn_decode(ctypes.byref(desc), ctypes.byref(cache.struct()), _ptr(q), _ptr(seq_lens),
+                                        _ptr(out), dt, _ptr(lse), B, max_len, _ptr(workspace), workspace.numel(),
+                                        _ptr(err), _stream(stream)), "dense_attn_decode")
+
+
+def dense_attn_prefill(desc: LayerDesc, cache: KVCache, q, cu_q, seq_lens, out, lse, max_len: int,
+                       workspace: torch.Tensor, q_start=None, err=None, stream=None) -> None:
+    """Chunks of tokens (sequence b: rows cu_q[b] .. cu_q[b+1]-1 of q [T, 16, 128])
+    over their sequence's entries: causal from position q_start[b] on (desc.ratio
+    tokens per entry), or over every entry without q_start."""
+    B = seq_lens.numel()
+    dt = _dense_checks(q, seq_lens, out, lse, workspace, err, B)
+    _on_gpu("cu_q", cu_q, (torch.int32,), (B + 1,))
+    _on_gpu("q_start", q_start, (torch.int32,), (B,), optional=True)
+    if cache.page_table.shape[0] < B:
+        raise ValueError(f"seq_lens: {B} sequences, the page table has {cache.page_table.shape[0]}")
+    _check(lib().csa2_dense_attn_prefill(ctypes.byref(desc), ctypes.byref(cache.struct()), _ptr(q), _ptr(cu_q),
+                                         _ptr(q_start), _ptr(seq_lens), _ptr(out), dt, _ptr(lse), B, q.shape[0],
+                                         max_len, _ptr(workspace), workspace.numel(), _ptr(err), _stream(stream)),
+           "dense_attn_prefill")
 
 
 def decode_layers(descs: list[LayerDesc], cache: KVCache, q_idx: list, w: list, q: list, swa_kv: list, seq_lens,

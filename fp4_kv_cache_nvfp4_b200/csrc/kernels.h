@@ -125,4 +125,19 @@ struct StageArgs {
 };
 cudaError_t launch_stage_rows(const StageArgs& a, int B, cudaStream_t stream);
 
+// Dense attention over every entry of the main KV (dense_attn.cu).
+struct DenseArgs {
+    csa2_kv_cache cache;
+    const uint16_t* q;        // [rows][16][128] bf16
+    const int32_t* cu_q;      // prefill: [B + 1]; decode: nullptr (row b is sequence b's token)
+    const int32_t* q_start;   // causal prefill: [B]; nullptr: every entry is seen
+    const int32_t* seq_lens;  // [B]
+    void* out;                // [rows][16][128] fp32 or bf16
+    float* lse;               // [rows][16]
+    int32_t* err;
+    int32_t B, T, max_len, ratio, page_shift;
+    bool out_bf16;
+};
+cudaError_t launch_dense_attn(const DenseArgs& a, char* ws, cudaStream_t stream);
+
 }  // namespace csa2

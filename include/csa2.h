@@ -327,6 +327,62 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
                                          float* lse, int32_t rows, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Dense attention over the FP4 main KV: every query token attends to every
+ * entry of its sequence that it may see, not to a selected set.  The pages
+ * have no counterpart to this call.  It serves what lies beside the sparse
+ * path: contexts of at most 512 entries, where both are the same attention;
+ * the dense layers a sparse model is trained and compared against; drafts of
+ * several tokens checked at once; queries over an encoder's entries.
+ *   k_j | v_j = e2m1(code) * e4m3(scale) of entry j (channels 0..127 | 128..255)
+ *   s_j = (q_h . k_j) / sqrt(128);  lse = log sum_j exp(s_j) (natural log)
+ *   out = sum_j exp(s_j - lse) v_j
+ * There is no window branch: csa2_attn_lse_merge joins an fp32 result with
+ * another one (a window's, another shard's).  Sums, maxima and partial
+ * results are held in fp32; the weights exp(s_j - max) are rounded to fp16
+ * (11 significant bits) for a bf16 result and carried as two fp16 terms (22
+ * bits) for an fp32 result.
+ *
+ * Decode: one token per sequence, which sees entries [0, seq_lens[b]).
+ *   q [B][16][128] bf16; out [B][16][128]; lse [B][16] fp32
+ * Prefill: sequence b's tokens are rows cu_q[b] .. cu_q[b+1]-1 (any number,
+ * none included) of q [T][16][128]; cu_q [B+1].
+ *   q_start [B]: token i of sequence b is at position q_start[b] + i (>= 0) and
+ *     sees the entries j < seq_lens[b] with (j+1)*ratio - 1 <= its position
+ *     (causal; the chunk's own entries are appended first);
+ *   q_start NULL: it sees all seq_lens[b] entries (cross attention to states
+ *     of another length).
+ *   out [T][16][128]; lse [T][16] fp32.  Rows outside every sequence's range
+ *   (behind cu_q[B], before cu_q[0]) are neither read nor written.
+ * Of desc the dimensions are checked and, for a causal prefill, ratio is used.
+ * out_dtype: CSA2_SRC_F32 or CSA2_SRC_BF16.  A token that sees no entry
+ * (length 0, or a causal mask that leaves none) gets out = 0, lse = -inf.
+ * What is not seen has no influence, whatever it holds (a NaN scale, a missing
+ * page).  Of an entry that is seen, a NaN scale among its 16 makes the results
+ * of the tokens that see it NaN.
+ * Detected on the device: a length outside [0, max_len] or a negative
+ * q_start (CSA2_DEV_LEN; the sequence counts as empty), a range of cu_q that
+ * is not ascending or not inside [0, T] (CSA2_DEV_LEN; that sequence's rows
+ * stay as they were), a missing page (CSA2_DEV_PAGE; its entries count as not
+ * seen).  Results do not vary from run to run.
+ * q and out must be 16-byte aligned, codes and scales in device memory
+ * (UNSUPPORTED if they are in host memory: these calls read them whole), the
+ * cache smaller than 2^31 slots, B <= 65536 and T <= 2^26 (UNSUPPORTED).
+ * max_len bounds seq_lens (1 <= max_len <= max_pages_per_seq * page_size).
+ * workspace: device memory of csa2_dense_attn_workspace_bytes() bytes, 256-byte
+ * aligned; what it holds before a call does not matter.  Calls sharing one
+ * workspace must not overlap on the GPU. */
+CSA2_API size_t csa2_dense_attn_workspace_bytes(const csa2_layer_desc* desc, int32_t B, int32_t prefill);
+CSA2_API csa2_status csa2_dense_attn_decode(const csa2_layer_desc* desc, const csa2_kv_cache* cache, const uint16_t* q,
+                                            const int32_t* seq_lens, void* out, int32_t out_dtype, float* lse,
+                                            int32_t B, int64_t max_len, void* workspace, size_t ws_bytes,
+                                            int32_t* err_word, void* stream);
+CSA2_API csa2_status csa2_dense_attn_prefill(const csa2_layer_desc* desc, const csa2_kv_cache* cache,
+                                             const uint16_t* q, const int32_t* cu_q, const int32_t* q_start,
+                                             const int32_t* seq_lens, void* out, int32_t out_dtype, float* lse,
+                                             int32_t B, int32_t T, int64_t max_len, void* workspace, size_t ws_bytes,
+                                             int32_t* err_word, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Allocation-free decode indexer.  The pages have no counterpart to this call:
  * it is an integration convenience for callers that cannot allocate device
  * memory where they run the indexer -- plug-ins whose host framework owns all
