@@ -87,6 +87,15 @@ def lib() -> ctypes.CDLL:
                                                   _P, _I32, _P, _I32, _I32, _I64, _P, _SZ, _P, _P]
             for n in ("csa2_dense_attn_decode", "csa2_dense_attn_prefill"):
                 getattr(L, n).restype = _I32
+            caches, i32p = ctypes.POINTER(_Cache), _P
+            L.csa2_kv_pages_workspace_bytes.argtypes = [_I64, _I32]
+            L.csa2_kv_pages_workspace_bytes.restype = _SZ
+            L.csa2_kv_pages_copy.argtypes = [_I32, caches, i32p, i32p, _I32, i32p, _P]
+            L.csa2_kv_pages_fork.argtypes = [_I32, caches, i32p, _I32, i32p, i32p, i32p, i32p, _I32, _P, _SZ, i32p, _P]
+            L.csa2_kv_pages_free.argtypes = [caches, i32p, _I32, i32p, i32p, i32p, _I32, i32p, _P]
+            L.csa2_kv_pages_compact.argtypes = [_I32, caches, i32p, _I32, i32p, i32p, i32p, _P, _SZ, i32p, _P]
+            for n in ("csa2_kv_pages_copy", "csa2_kv_pages_fork", "csa2_kv_pages_free", "csa2_kv_pages_compact"):
+                getattr(L, n).restype = _I32
             L.csa2_swa_replay.argtypes = [_P, _P, _P, _P, _I32, _I32, _I32, _P, _P]
             L.csa2_swa_replay.restype = _I32
             L.csa2_test_empty_chain.argtypes = [_I32, _I32, _I32, _P, _P]
@@ -357,6 +366,75 @@ def dense_attn_prefill(desc: LayerDesc, cache: KVCache, q, cu_q, seq_lens, out, 
                                          _ptr(q_start), _ptr(seq_lens), _ptr(out), dt, _ptr(lse), B, q.shape[0],
                                          max_len, _ptr(workspace), workspace.numel(), _ptr(err), _stream(stream)),
            "dense_attn_prefill")
+
+
+def kv_pages_workspace_bytes(n_phys_pages: int, n: int = 0) -> int:
+    """Workspace of n forks (or, with n = 0, of a compaction) over that many pages."""
+    size = int(lib().csa2_kv_pages_workspace_bytes(n_phys_pages, n))
+    if size == 0:
+        raise ValueError(f"{n_phys_pages} pages and {n} forks: out of range")
+    return size
+
+
+def _page_args(caches, refs, seq_lens, err):
+    """The caches as a C array, and their common table."""
+    if not caches:
+        raise ValueError("caches: empty")
+    c0 = caches[0]
+    for c in caches[1:]:
+        if c.page_table.data_ptr() != c0.page_table.data_ptr() or c.page_table.shape != c0.page_table.shape:
+            raise ValueError("caches: they do not share one page table")
+    _on_gpu("page_table", c0.page_table, (torch.int32,), (None, None))
+    _on_gpu("refs", refs, (torch.int32,), (c0.n_phys_pages,))
+    _on_gpu("seq_lens", seq_lens, (torch.int32,), (c0.page_table.shape[0],), optional=True)
+    _on_gpu("err", err, (torch.int32,), (1,), optional=True)
+    return (_Cache * len(caches))(*[c.struct() for c in caches]), c0.page_table
+
+
+def kv_pages_copy(caches: list[KVCache], src, dst, err=None, stream=None) -> None:
+    """Physical pages src[i] -> dst[i] in every cache (int32; a -1 skips the pair)."""
+    _on_gpu("src", src, (torch.int32,), (None,))
+    _on_gpu("dst", dst, (torch.int32,), (src.numel(),))
+    _on_gpu("err", err, (torch.int32,), (1,), optional=True)
+    if not caches:
+        raise ValueError("caches: empty")
+    C = (_Cache * len(caches))(*[c.struct() for c in caches])
+    _check(lib().csa2_kv_pages_copy(len(caches), C, _ptr(src), _ptr(dst), src.numel(), _ptr(err), _stream(stream)),
+           "kv_pages_copy")
+
+
+def kv_pages_fork(caches: list[KVCache], refs, seq_lens, parents, children, workspace: torch.Tensor, err=None,
+                  stream=None) -> None:
+    """Rows children[i] of the caches' page table share what rows parents[i] hold."""
+    C, table = _page_args(caches, refs, seq_lens, err)
+    _on_gpu("parents", parents, (torch.int32,), (None,))
+    _on_gpu("children", children, (torch.int32,), (parents.numel(),))
+    _on_gpu("workspace", workspace, (torch.uint8,), (None,))
+    _check(lib().csa2_kv_pages_fork(len(caches), C, _ptr(table), table.shape[0], _ptr(refs), _ptr(seq_lens),
+                                    _ptr(parents), _ptr(children), parents.numel(), _ptr(workspace),
+                                    workspace.numel(), _ptr(err), _stream(stream)), "kv_pages_fork")
+
+
+def kv_pages_free(cache: KVCache, refs, seq_lens, seqs, err=None, stream=None) -> None:
+    """Rows seqs[i] of the page table become free; their pages lose one holder each."""
+    C, table = _page_args([cache], refs, seq_lens, err)
+    _on_gpu("seqs", seqs, (torch.int32,), (None,))
+    _check(lib().csa2_kv_pages_free(C, _ptr(table), table.shape[0], _ptr(refs), _ptr(seq_lens), _ptr(seqs),
+                                    seqs.numel(), _ptr(err), _stream(stream)), "kv_pages_free")
+
+
+def kv_pages_compact(caches: list[KVCache], refs, page_map, n_live, workspace: torch.Tensor, err=None,
+                     stream=None) -> None:
+    """Live pages move into the free numbers below their count; the page table and
+    refs follow, page_map [n_phys_pages] tells each page's new number (-1: free)
+    and n_live [1] their count."""
+    C, table = _page_args(caches, refs, None, err)
+    _on_gpu("page_map", page_map, (torch.int32,), (caches[0].n_phys_pages,))
+    _on_gpu("n_live", n_live, (torch.int32,), (1,))
+    _on_gpu("workspace", workspace, (torch.uint8,), (None,))
+    _check(lib().csa2_kv_pages_compact(len(caches), C, _ptr(table), table.shape[0], _ptr(refs), _ptr(page_map),
+                                       _ptr(n_live), _ptr(workspace), workspace.numel(), _ptr(err), _stream(stream)),
+           "kv_pages_compact")
 
 
 def decode_layers(descs: list[LayerDesc], cache: KVCache, q_idx: list, w: list, q: list, swa_kv: list, seq_lens,

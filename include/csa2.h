@@ -73,6 +73,8 @@ typedef enum {
 #define CSA2_DEV_ALIGN 0x20   /* a kernel's dynamic shared memory was not aligned as its
                                * layout needs; the kernel returned without computing */
 
+#define CSA2_DEV_POOL 0x40    /* no free page left: a requested fork was not made */
+
 typedef enum { CSA2_MODE_FULL = 0, CSA2_MODE_REINDEX = 1, CSA2_MODE_REUSE = 2 } csa2_mode;
 typedef enum { CSA2_LEVEL_BLOCK = 0, CSA2_LEVEL_TOKEN = 1 } csa2_level;
 typedef enum { CSA2_SRC_F32 = 0, CSA2_SRC_BF16 = 1 } csa2_src_dtype;
@@ -381,6 +383,64 @@ CSA2_API csa2_status csa2_dense_attn_prefill(const csa2_layer_desc* desc, const 
                                              const int32_t* seq_lens, void* out, int32_t out_dtype, float* lse,
                                              int32_t B, int32_t T, int64_t max_len, void* workspace, size_t ws_bytes,
                                              int32_t* err_word, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* The pages of a paged cache: copy, fork, free, compact.  The pages this
+ * method is described on have no counterpart; they only say that prefixes are
+ * kept and reused.  The caller keeps, in device memory:
+ *   caches      n_caches caches (HOST array; 1 to 16, each with its own arrays)
+ *               whose pages share one numbering and one table: a model's
+ *               Full layers.  page_size, max_pages_per_seq and n_phys_pages
+ *               (<= 2^22) must be equal; codes and scales, and idx_k and
+ *               idx_k_pooled where they are not NULL, are copied
+ *   page_table  [n_seqs][max_pages_per_seq] int32, -1 where there is no page
+ *               (rewritten by these calls; the caches' own page_table is not read)
+ *   refs        [n_phys_pages] int32, 16-byte aligned: how many entries of the
+ *               page table hold the page; 0: free
+ *   seq_lens    [n_seqs] int32 entries; 0: the row is free
+ * The counts are the allocator: a new page is the free one with the lowest
+ * number.  Results do not vary from run to run.
+ *
+ * copy: page src[i] -> dst[i] in every cache, for i < n; a pair with a -1 is
+ *   skipped, one out of range is skipped and reported (CSA2_DEV_PAGE).  The
+ *   counts are not read.  A page that is written by one pair must not appear in
+ *   another pair (its content would be undefined).
+ * fork: row children[i] becomes a second holder of what row parents[i] holds:
+ *   full pages are shared (their counts go up by one), a partly filled last page is copied
+ *   into a new one, so both may append; pages behind the parent's length are
+ *   not taken over.  New pages go to the requests in their order.  n <= 1024;
+ *   (-1, -1) is skipped.  Not made, and reported: a row out of range, a child
+ *   whose row is in use, that an earlier request names as its child, or that is some
+ *   request's parent (CSA2_DEV_SLOT); a parent's bad length (CSA2_DEV_LEN) or
+ *   missing last page (CSA2_DEV_PAGE); a partial page when none is free (CSA2_DEV_POOL).  A
+ *   missing page among the full ones is -1 in the child too (CSA2_DEV_PAGE).
+ * free: rows seqs[i] become free: each page they hold loses one holder.  -1 is
+ *   skipped, a row listed twice is freed once.  A row out of range is reported
+ *   (CSA2_DEV_SLOT), as is a page out of range or held more often than counted
+ *   (CSA2_DEV_PAGE; its count stays 0).
+ * compact: with n live pages (count > 0), the live ones numbered n and above
+ *   move to the free numbers below n, lowest to lowest, in every cache; table
+ *   and counts follow.  page_map [n_phys_pages] receives each page's new number
+ *   (-1: it was free), n_live [1] receives n.  A table entry that names no live page becomes
+ *   -1 (CSA2_DEV_PAGE).  The freed pages keep their old bytes.
+ * Calls that use these arrays must not overlap on the GPU with one another or
+ * with a call that reads or appends to the caches.
+ * workspace (fork, compact): csa2_kv_pages_workspace_bytes(n_phys_pages, n)
+ * bytes (n: forks; 0 for compact), 256-byte aligned; what it holds before a
+ * call does not matter.  0 is returned for sizes out of range. */
+CSA2_API size_t csa2_kv_pages_workspace_bytes(int64_t n_phys_pages, int32_t n);
+CSA2_API csa2_status csa2_kv_pages_copy(int32_t n_caches, const csa2_kv_cache* caches, const int32_t* src,
+                                        const int32_t* dst, int32_t n, int32_t* err_word, void* stream);
+CSA2_API csa2_status csa2_kv_pages_fork(int32_t n_caches, const csa2_kv_cache* caches, int32_t* page_table,
+                                        int32_t n_seqs, int32_t* refs, int32_t* seq_lens, const int32_t* parents,
+                                        const int32_t* children, int32_t n, void* workspace, size_t ws_bytes,
+                                        int32_t* err_word, void* stream);
+CSA2_API csa2_status csa2_kv_pages_free(const csa2_kv_cache* cache, int32_t* page_table, int32_t n_seqs, int32_t* refs,
+                                        int32_t* seq_lens, const int32_t* seqs, int32_t n, int32_t* err_word,
+                                        void* stream);
+CSA2_API csa2_status csa2_kv_pages_compact(int32_t n_caches, const csa2_kv_cache* caches, int32_t* page_table,
+                                           int32_t n_seqs, int32_t* refs, int32_t* page_map, int32_t* n_live,
+                                           void* workspace, size_t ws_bytes, int32_t* err_word, void* stream);
 
 /* ---------------------------------------------------------------------- */
 /* Allocation-free decode indexer.  The pages have no counterpart to this call:
