@@ -256,6 +256,23 @@ __device__ __forceinline__ uint32_t f2_to_h2(float lo, float hi) {
     return d;
 }
 
+// --- mma.sync and 2^x -------------------------------------------------------------
+// D[16 x 8] += A[16 x 16] . B[16 x 8], fp16 inputs, fp32 accumulators
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 2^x, the hardware approximation (error below 2^-22; subnormal results become 0)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // --- warp / block scans ------------------------------------------------------------
 __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t v) {
     int lane = threadIdx.x & 31;

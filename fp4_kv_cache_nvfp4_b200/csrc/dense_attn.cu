@@ -138,7 +138,7 @@ csa2_status dense_args(const csa2_layer_desc* desc, const csa2_kv_cache* cache, 
         return CSA2_ERR_INVALID_ARG;
     if (max_len > (int64_t)cache->max_pages_per_seq * cache->page_size) return CSA2_ERR_INVALID_ARG;
     if (B > kMaxDenseSeqs || rows > kMaxDenseRows || max_len > INT32_MAX - 65536 ||
-        cache->n_phys_pages * cache->page_size > INT32_MAX)
+        cache->n_phys_pages * cache->page_size > INT32_MAX || B * ((max_len + 127) / 128) > INT32_MAX)
         return CSA2_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256) || ws_bytes < csa2_dense_attn_workspace_bytes(desc, B, prefill))
         return CSA2_ERR_WORKSPACE;
@@ -168,8 +168,7 @@ extern "C" {
 
 size_t csa2_dense_attn_workspace_bytes(const csa2_layer_desc* desc, int32_t B, int32_t prefill) {
     if (!desc || B < 0) return 0;
-    (void)prefill;
-    return 256;
+    return prefill ? 256 : (dense_decode_ws_bytes() + 255) & ~size_t(255);
 }
 
 csa2_status csa2_dense_attn_decode(const csa2_layer_desc* desc, const csa2_kv_cache* cache, const uint16_t* q,
@@ -180,7 +179,7 @@ csa2_status csa2_dense_attn_decode(const csa2_layer_desc* desc, const csa2_kv_ca
     csa2_status s = dense_args(desc, cache, q, seq_lens, out, out_dtype, lse, B, B, max_len, workspace, ws_bytes, 0,
                                err_word, a);
     if (s != CSA2_OK || B == 0) return s;
-    return from_cuda(launch_dense_attn(a, static_cast<char*>(workspace), (cudaStream_t)stream));
+    return from_cuda(launch_dense_decode(a, static_cast<char*>(workspace), (cudaStream_t)stream));
 }
 
 csa2_status csa2_dense_attn_prefill(const csa2_layer_desc* desc, const csa2_kv_cache* cache, const uint16_t* q,

@@ -139,5 +139,8 @@ struct DenseArgs {
     bool out_bf16;
 };
 cudaError_t launch_dense_attn(const DenseArgs& a, char* ws, cudaStream_t stream);
+// One token per sequence (dense_decode.cu).
+size_t dense_decode_ws_bytes();
+cudaError_t launch_dense_decode(const DenseArgs& a, char* ws, cudaStream_t stream);
 
 }  // namespace csa2

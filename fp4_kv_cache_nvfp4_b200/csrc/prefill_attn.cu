@@ -87,13 +87,6 @@ static_assert(PT_SMEM <= 227 * 1024, "K7 shared memory");
 constexpr uint32_t kPtWaitLimit = 1u << 22;
 constexpr uint32_t PT_TMEM_COLS = 128 * PT_NTB;
 
-// Shared-memory descriptor of an MN-major, 128-byte-swizzled operand: rows of
-// 128 B (64 M-elements of one K index), 8-row groups SBO = 1024 B apart along
-// K, 64-element M groups `lbo` bytes apart.
-__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
 // D[128 x 16] (+)= A . B^T with fp16 operands, fp32 accumulators; a_mn: A is MN-major
 __device__ __forceinline__ void umma_f16(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t acc, bool a_mn) {
     const uint32_t idesc = (1u << 4) | (a_mn ? (1u << 15) : 0u) | ((uint32_t)(16 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -109,13 +102,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&v)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "r"(addr));
-}
-
-// 2^x (the hardware approximation; P is rounded to fp16 afterwards)
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // 8 dims (one 16-byte chunk ch of the 16 of a K or V row) of a bf16 window row

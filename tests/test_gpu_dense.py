@@ -124,15 +124,21 @@ def test_decode_bad_lengths_and_pages(csa2):
         check(out[b:b + 1], lse[b:b + 1], reference(q[b:b + 1], c.rows(b), [lens[b]], gone[b]), f"seq {b}")
 
 
-def test_decode_a_nan_entry_is_its_sequences_alone(csa2):
+@pytest.mark.parametrize("block", [0, 7, 8, 12])
+def test_decode_a_nan_entry_is_its_sequences_alone(csa2, block):
+    """A NaN scale of K reaches the whole row, one of V at least its own 16 dims."""
     lens = [100, 100]
     c = DenseCase(csa2, lens, 64, seed=2)
-    c.scales[c.slots(0, 100)[50], 12] = 0x7F
+    c.scales[c.slots(0, 100)[50], block] = 0x7F
     c.upload()
     q = queries(2)
-    out, lse, _ = decode(csa2, c, q, torch.bfloat16)
-    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
-    check(out[1:], lse[1:], reference(q[1:], c.rows(1), [100]), "the other sequence")
+    for dt in DT.values():
+        out, lse, _ = decode(csa2, c, q, dt)
+        if block < 8:
+            assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+        else:
+            assert torch.isnan(out[0, :, 16 * (block - 8):16 * (block - 7)]).all()
+        check(out[1:], lse[1:], reference(q[1:], c.rows(1), [100]), "the other sequence")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -206,7 +212,10 @@ def test_prefill_a_nan_entry_reaches_those_who_see_it(csa2):
             out, lse, _ = prefill(csa2, c, q, [0, 20], dt, [130])
             clean = DenseCase(csa2, [150], 64, seed=2)
             check(out[:10], lse[:10], reference(q[:10], clean.rows(0), seen_of(150, 10, 130, 1)), "who do not see it")
-            assert torch.isnan(out[10:]).all() and torch.isnan(lse[10:]).all()
+            if ch < 8:
+                assert torch.isnan(out[10:]).all() and torch.isnan(lse[10:]).all()
+            else:
+                assert torch.isnan(out[10:, :, 16 * (ch - 8):16 * (ch - 7)]).all()
 
 
 @pytest.mark.parametrize("gain", [1e-30, 8.0, 1e4])
@@ -259,7 +268,7 @@ def test_captured_and_replayed_with_new_inputs(csa2):
     sl, cu, st = i32(lens), i32([0, 10, 20, 30]), i32([890, 30, 1990])
     out, lse = torch.empty((3, 16, 128), device="cuda"), torch.empty((3, 16), device="cuda")
     outp, lsep = torch.empty((30, 16, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((30, 16), device="cuda")
-    ws = torch.empty(csa2.dense_attn_workspace_bytes(d, 3, True), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(csa2.dense_attn_workspace_bytes(d, 3, p) for p in (False, True)), dtype=torch.uint8, device="cuda")
 
     def both():
         csa2.dense_attn_decode(d, c.cache, q, sl, out, lse, c.max_len, ws)
