@@ -46,10 +46,11 @@ __device__ __forceinline__ float quad_max(float v) {
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
-// two E4M3 bytes -> f16x2 (byte 0 in the low half)
+// two E4M3 bytes (the low half of b2) -> f16x2, byte 0 in the low half
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t b2) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)b2, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    uint32_t d;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(d) : "r"(b2));
+    return d;
 }
 
 // fp16 pair of what the fp16 pair `h` leaves of (lo, hi): together 22 bits
@@ -81,14 +82,15 @@ __device__ __forceinline__ void dense_store(const DenseArgs& a, int64_t row, int
     if (d8 == 0) a.lse[row] = l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * 0.6931471805599453f;
 }
 
-// Tensor map of the code rows: boxes of min(page, tile) rows of 128 bytes, the
+// Tensor map of the code rows: boxes of min(page, 64) rows of 128 bytes, the
 // box's innermost coordinate always 0.
-static bool dense_code_map(const csa2_kv_cache& cache, CUtensorMap* map, int tile) {
+constexpr int kDenseBoxShift = 6;
+static bool dense_code_map(const csa2_kv_cache& cache, CUtensorMap* map) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)kCodeBytes, (cuuint64_t)(cache.n_phys_pages * cache.page_size)};
     const cuuint64_t strides[1] = {(cuuint64_t)kCodeBytes};
-    const cuuint32_t box[2] = {(cuuint32_t)kCodeBytes, (cuuint32_t)std::min(tile, cache.page_size)};
+    const cuuint32_t box[2] = {(cuuint32_t)kCodeBytes, (cuuint32_t)std::min(1 << kDenseBoxShift, cache.page_size)};
     const cuuint32_t estr[2] = {1u, 1u};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)cache.codes, dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

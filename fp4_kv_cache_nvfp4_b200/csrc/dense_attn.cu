@@ -138,7 +138,7 @@ csa2_status dense_args(const csa2_layer_desc* desc, const csa2_kv_cache* cache, 
         return CSA2_ERR_INVALID_ARG;
     if (max_len > (int64_t)cache->max_pages_per_seq * cache->page_size) return CSA2_ERR_INVALID_ARG;
     if (B > kMaxDenseSeqs || rows > kMaxDenseRows || max_len > INT32_MAX - 65536 ||
-        cache->n_phys_pages * cache->page_size > INT32_MAX || B * ((max_len + 127) / 128) > INT32_MAX)
+        cache->n_phys_pages * cache->page_size > INT32_MAX || B * ((max_len + 63) / 64) > INT32_MAX)
         return CSA2_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256) || ws_bytes < csa2_dense_attn_workspace_bytes(desc, B, prefill))
         return CSA2_ERR_WORKSPACE;
