@@ -1,0 +1,695 @@
+// Dense prefill attention on the 5th-generation tensor cores (tcgen05): ragged
+// chunks of query tokens over every entry of the FP4 main KV that they see.
+//
+// Mathematics as in decode: one pass over the entries with a running maximum
+// and sum per row, the maximum following lazily (see dense_decode.cu).  A row
+// is a (token, head) pair: the 16 heads share K and V, so 8 tokens fill the 128
+// rows of a product,
+//   S[128 x 128 entries] = Q . K^T,   O[128 x 128 dims] += P . V.
+//
+// A work unit is 16 tokens (two 128-row tiles) over its tiles of 128 entries.
+// The tiles of all units form one list, of which every CTA (one per SM) takes an
+// equal contiguous share, whatever the lengths and masks; a unit that spans
+// CTAs leaves partial results that a second kernel joins.  In a CTA
+//   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread per row: maximum,
+//                   P = 2^(S c - m) as fp16 back into TMEM over S, the sum;
+//                   O's rescaling when m rises (rare); the result's rows
+//   warps 8-15      K and V of the next tiles: FP4 read with plain loads one tile
+//                   ahead, dequantised to fp16 (exact) into swizzled shared tiles
+//   warp 16         issues the products: while one row tile is in its softmax, the
+//                   other's products run
+// TMEM: S of both row tiles (P over them), O of both: all 512 columns.
+//
+// What bounds it: per (row tile, entry tile) the products take 1024 cycles of the
+// tensor core, the 16,384 exponentials 1024 cycles of the special-function
+// units, and the products' operands with the dequantised tiles' writes about 1000
+// cycles of shared memory, so three units are near their limits at once.
+#include <algorithm>
+
+#include "common.cuh"
+#include "dense.cuh"
+#include "kernels.h"
+#include "tc.cuh"
+
+namespace csa2 {
+
+constexpr int DP_TOK = 16;                       // tokens per unit (8 per row tile)
+constexpr int DP_ROWS = DP_TOK * kH;             // 256
+constexpr int DP_KEYS = 128;                     // entries per tile
+constexpr uint32_t DP_HALF = 128 * 128;          // 64 channels of an operand tile: [128 rows][128 B], swizzled
+constexpr uint32_t DP_TILE = 2 * DP_HALF;        // 32 KiB
+constexpr int DP_W_CONV = 8, DP_NCONV = 8, DP_W_MMA = 16, DP_WARPS = 17;
+constexpr int DP_THREADS = DP_WARPS * 32;
+constexpr size_t DP_OFF_Q = 0;                            // [2 row tiles]
+constexpr size_t DP_OFF_K = DP_OFF_Q + 2 * DP_TILE;       // [2 slots]
+constexpr size_t DP_OFF_V = DP_OFF_K + 2 * DP_TILE;       // [2 slots]
+constexpr size_t DP_OFF_OK = DP_OFF_V + 2 * DP_TILE;      // [4][16 B]: one bit per entry of a K tile, 0: missing page
+constexpr size_t DP_OFF_BAR = DP_OFF_OK + 64;
+constexpr int DP_NBAR = 4 * 2 + 4 * 2 + 1;
+constexpr size_t DP_OFF_SCAN = DP_OFF_BAR + DP_NBAR * 8;  // [64] words
+constexpr size_t DP_OFF_MISC = DP_OFF_SCAN + 256;         // tmem base, timeout flag, start sequence, unit, its first tile
+constexpr size_t DP_SMEM = DP_OFF_MISC + 32 + 1024;       // + slack for the 1 KiB alignment
+static_assert(DP_OFF_BAR % 8 == 0 && DP_SMEM <= 227 * 1024, "dense prefill layout");
+constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdescS | (1u << 16);  // B (V) has its dims contiguous
+
+struct PrefillDenseArgs {
+    DenseArgs a;
+    float* part_o;  // [2 * ctas][256 rows][128], times 2^(kPBias - m)
+    float* part_m;  // [2 * ctas][256]
+    float* part_l;  // [2 * ctas][256]
+    int4* cut;      // [2 * ctas]: (first row token, tokens, first tile, end), (first tile of this CTA) of the unit it begins inside
+};
+
+// ---- which units and tiles ----------------------------------------------------------
+// One sequence's queries: tokens [row0, row0 + nq), the first at position p0.
+struct SeqQ {
+    int row0, nq, len;
+    int64_t p0;
+    __device__ __forceinline__ int units() const { return (nq + DP_TOK - 1) / DP_TOK; }
+};
+__device__ __forceinline__ SeqQ seq_q(const DenseArgs& a, int b, bool report) {
+    SeqQ s;
+    const int lo = __ldg(a.cu_q + b), hi = __ldg(a.cu_q + b + 1);
+    const bool range = lo >= 0 && hi >= lo && hi <= a.T;
+    s.row0 = lo;
+    s.nq = range ? hi - lo : 0;
+    s.len = __ldg(a.seq_lens + b);
+    s.p0 = a.q_start ? __ldg(a.q_start + b) : 0;
+    const bool bad = s.len < 0 || s.len > a.max_len || s.p0 < 0;
+    if (report && (!range || bad)) dev_error(a.err, CSA2_DEV_LEN);
+    if (bad) {
+        s.len = 0;
+        s.p0 = 0;
+    }
+    return s;
+}
+// Entries that the token `i` of the sequence sees
+__device__ __forceinline__ int seen_by(const DenseArgs& a, const SeqQ& s, int i) {
+    if (!a.q_start) return s.len;
+    const int64_t v = (s.p0 + i + 1) >> (a.ratio - 1);
+    return v < s.len ? (int)v : s.len;
+}
+// Tiles of unit k: those its last token sees, one at least (it writes the rows)
+__device__ __forceinline__ uint32_t unit_tiles(const DenseArgs& a, const SeqQ& s, int k) {
+    return max(1u, (uint32_t)(seen_by(a, s, min((k + 1) * DP_TOK, s.nq) - 1) + DP_KEYS - 1) / DP_KEYS);
+}
+// Tiles of the units before k.  With A = p0 + 16 + 127 r and D = 128 r, a full
+// unit i has min(C, floor((A + 16 i) / D)) tiles, C = ceil(len / 128): a staircase,
+// whose sum is a difference of G(x) = sum_{j < x} floor(j / (8 r)).
+__device__ __forceinline__ uint64_t tiles_before(const DenseArgs& a, const SeqQ& s, int k) {
+    if (k <= 0) return 0;
+    const int last = s.units() - 1;
+    const uint64_t C = max(1u, (uint32_t)(s.len + DP_KEYS - 1) / DP_KEYS);
+    const int m = min(k, last);  // full units
+    uint64_t n;
+    if (!a.q_start) {
+        n = (uint64_t)m * C;
+    } else {
+        const int64_t r = a.ratio, A = s.p0 + DP_TOK + 127 * r, D = 128 * r, M = D / DP_TOK, x = A / DP_TOK;
+        int64_t ic = ((int64_t)C * D - A + DP_TOK - 1) / DP_TOK;  // the first unit with C
+        ic = ic < 0 ? 0 : ic > m ? m : ic;
+        auto G = [&](int64_t v) {
+            const int64_t q = v / M;
+            return M * (q * (q - 1) / 2) + q * (v - q * M);
+        };
+        n = (uint64_t)(G(x + ic) - G(x)) + (uint64_t)(m - ic) * C;
+    }
+    return k > last ? n + unit_tiles(a, s, last) : n;
+}
+
+// Walks the units of a CTA's share in order.
+struct Walk {
+    int b, k, nk;
+    SeqQ s;
+    uint32_t t0, t1;  // the unit's tiles in the flattened list
+    __device__ __forceinline__ void start(const DenseArgs& a, const uint32_t* at) {
+        b = (int)at[0];
+        k = (int)at[1];
+        t0 = at[2];
+        s = seq_q(a, b, false);
+        nk = s.units();
+        t1 = t0 + unit_tiles(a, s, k);
+    }
+    __device__ __forceinline__ void next(const DenseArgs& a) {
+        t0 = t1;
+        if (++k >= nk) {
+            k = 0;
+            do {
+                s = seq_q(a, ++b, false);
+                nk = s.units();
+            } while (nk == 0 && b + 1 < a.B);
+        }
+        t1 = t0 + unit_tiles(a, s, k);
+    }
+    __device__ __forceinline__ int tokens() const { return min(DP_TOK, s.nq - k * DP_TOK); }
+};
+
+// ---- tensor-core helpers --------------------------------------------------------------
+// D[128 x 128] (+)= A . B with fp16 operands, A in shared memory
+__device__ __forceinline__ void dp_mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(kIdescS), "r"(acc), "r"(0u)
+        : "memory");
+}
+// the same with A in TMEM (rows = lanes, two fp16 per column) and B transposed
+__device__ __forceinline__ void dp_mma_ts(uint32_t d, uint32_t ta, uint64_t db, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
+        "r"(ta), "l"(db), "r"(kIdescPV), "r"(acc), "r"(0u)
+        : "memory");
+}
+// 32 consecutive columns of this thread's lane
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// SPLIT: P as two fp16 terms (fp32 results)
+template <bool SPLIT>
+__global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const PrefillDenseArgs d) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const DenseArgs& a = d.a;
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + DP_OFF_BAR);  // [2] K tile written (converter warps)
+    uint64_t* kempty = kfull + 2;                                      // [2] read by the products (commit)
+    uint64_t* vfull = kempty + 2;
+    uint64_t* vempty = vfull + 2;
+    uint64_t* qfull = vempty + 2;   // [2] a row tile's Q written (4 softmax warps)
+    uint64_t* sfull = qfull + 2;    // [2] S complete (commit)
+    uint64_t* pfull = sfull + 2;    // [2] P written, O rescaled (4 softmax warps)
+    uint64_t* ofull = pfull + 2;    // [2] O of a unit complete (commit)
+    uint64_t* mma_done = ofull + 2;
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem + DP_OFF_MISC);
+    volatile uint32_t* s_timeout = misc + 1;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&kfull[i], DP_NCONV);
+            mbar_init(&kempty[i], 1);
+            mbar_init(&vfull[i], DP_NCONV);
+            mbar_init(&vempty[i], 1);
+            mbar_init(&qfull[i], 4);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+            mbar_init(&ofull[i], 1);
+        }
+        mbar_init(mma_done, 1);
+        *s_timeout = 0;
+        fence_mbar_init();
+    }
+    if (wid == DP_W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(misc)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this CTA's share of the tiles: [lo, hi) of the flattened list ------------
+    const int per_thread = (a.B + DP_THREADS - 1) / DP_THREADS;
+    const int b0 = min(a.B, tid * per_thread), b1 = min(a.B, b0 + per_thread);
+    uint32_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const SeqQ s = seq_q(a, b, blockIdx.x == 0);
+        mine += (uint32_t)tiles_before(a, s, s.units());
+    }
+    uint32_t total;
+    const uint32_t before = block_excl_scan(mine, reinterpret_cast<uint32_t*>(smem + DP_OFF_SCAN), &total);
+    const uint32_t per = (total + gridDim.x - 1) / gridDim.x;
+    const uint32_t lo = min(total, per * blockIdx.x), hi = min(total, lo + per);
+    if (lo < hi && lo >= before && lo < before + mine) {
+        uint32_t t = before;
+        for (int b = b0; b < b1; ++b) {
+            const SeqQ s = seq_q(a, b, false);
+            const uint32_t n = (uint32_t)tiles_before(a, s, s.units());
+            if (lo < t + n) {
+                int k0 = 0, k1 = s.units();  // the last unit whose first tile is not behind lo
+                while (k1 - k0 > 1) {
+                    const int k = (k0 + k1) / 2;
+                    if (tiles_before(a, s, k) <= lo - t) k0 = k;
+                    else k1 = k;
+                }
+                misc[2] = (uint32_t)b;
+                misc[3] = (uint32_t)k0;
+                misc[4] = t + (uint32_t)tiles_before(a, s, k0);
+                break;
+            }
+            t += n;
+        }
+    }
+    __syncthreads();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; after one timeout every wait returns at once
+        if (*s_timeout) return;
+        if (!mbar_wait(bar, parity, kDenseWaitLimit)) *s_timeout = 1;
+    };
+
+    if (lo < hi && wid == DP_W_MMA) {
+        // ================= the products =================
+        if (lane == 0) {
+            Walk w;
+            w.start(a, misc + 2);
+            uint32_t kn = 0, vn = 0, seg = 0, seg1 = 0, pn[2] = {0, 0};  // tiles, units (with a second row tile), P tiles so far
+            const uint32_t qaddr = smem_u32(smem + DP_OFF_Q), kaddr = smem_u32(smem + DP_OFF_K), vaddr = smem_u32(smem + DP_OFF_V);
+            auto mma_s = [&](int i) {  // S of row tile i over K tile kn
+                const uint32_t q = qaddr + (uint32_t)i * DP_TILE, k = kaddr + (kn & 1u) * DP_TILE;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    dp_mma_ss(tmem + 128u * i, umma_desc_sw128(q + (ks >> 2) * DP_HALF) + 2u * (ks & 3),
+                              umma_desc_sw128(k + (ks >> 2) * DP_HALF) + 2u * (ks & 3), ks > 0);
+                umma_commit(&sfull[i]);
+            };
+            auto mma_pv = [&](int i, bool first) {  // O of row tile i += P . V tile vn
+                wait(&pfull[i], pn[i] & 1u);
+                ++pn[i];
+                tc_fence_after();
+                const uint32_t v = vaddr + (vn & 1u) * DP_TILE, p = tmem + 128u * i, o = tmem + 256u + 128u * i;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {  // P of 16 entries: 8 columns
+                    const uint64_t db = umma_desc_sw128_mn(v + ks * 2048u, DP_HALF);
+                    dp_mma_ts(o, p + 32u * (ks >> 1) + 8u * (ks & 1), db, !(first && ks == 0));
+                    if (SPLIT) dp_mma_ts(o, p + 32u * (ks >> 1) + 16u + 8u * (ks & 1), db, 1);
+                }
+            };
+            for (uint32_t t = lo; t < hi;) {
+                const uint32_t end = min(hi, w.t1);
+                const bool two = w.tokens() > DP_TOK / 2;
+                wait(&qfull[0], seg & 1u);
+                if (two) wait(&qfull[1], seg1 & 1u);
+                wait(&kfull[kn & 1u], (kn >> 1) & 1u);
+                tc_fence_after();
+                mma_s(0);
+                if (two) mma_s(1);
+                umma_commit(&kempty[kn & 1u]);
+                ++kn;
+                for (const uint32_t first = t; t < end; ++t) {
+                    const bool more = t + 1 < end;
+                    wait(&vfull[vn & 1u], (vn >> 1) & 1u);
+                    mma_pv(0, t == first);
+                    if (more) {
+                        wait(&kfull[kn & 1u], (kn >> 1) & 1u);
+                        tc_fence_after();
+                        mma_s(0);
+                    } else {
+                        umma_commit(&ofull[0]);
+                    }
+                    if (two) mma_pv(1, t == first);
+                    umma_commit(&vempty[vn & 1u]);
+                    ++vn;
+                    if (more) {
+                        if (two) mma_s(1);
+                        umma_commit(&kempty[kn & 1u]);
+                        ++kn;
+                    } else if (two) {
+                        umma_commit(&ofull[1]);
+                    }
+                }
+                ++seg;
+                seg1 += two;
+                if (t < hi) w.next(a);
+            }
+            umma_commit(mma_done);
+            if (!mbar_wait(mma_done, 0u, kDenseWaitLimit)) *s_timeout = 1;
+        }
+        __syncwarp();
+    } else if (lo < hi && wid >= DP_W_CONV) {
+        // ================= converters: FP4 rows -> fp16 operand tiles =================
+        // Thread ct owns quarter qt (32 channels of K and of V) of entries e0 and e0 + 64.
+        const int ct = tid - DP_W_CONV * 32, qt = ct & 3, e0 = ct >> 2, cw = wid - DP_W_CONV;
+        Walk w;
+        w.start(a, misc + 2);
+        struct Row {
+            uint4 k, v, s;  // codes of the quarter, the entry's 16 scales (zeros: not there)
+        };
+        auto fetch = [&](uint32_t t, Row (&R)[2], uint32_t& missing) {
+            missing = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int pos = (int)(t - w.t0) * DP_KEYS + e0 + 64 * i;
+                R[i].k = R[i].v = R[i].s = make_uint4(0, 0, 0, 0);
+                if (pos < w.s.len) {
+                    const int64_t slot = entry_slot(a.cache, a.page_shift, w.b, pos, a.err);
+                    if (slot >= 0) {
+                        const uint4* c = reinterpret_cast<const uint4*>(a.cache.codes + slot * kCodeBytes);
+                        R[i].k = __ldg(c + qt);
+                        R[i].v = __ldg(c + 4 + qt);
+                        R[i].s = __ldg(reinterpret_cast<const uint4*>(a.cache.scales + slot * kScales));
+                    } else {
+                        missing |= 1u << i;
+                    }
+                }
+            }
+        };
+        auto word = [](const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+        auto nan_bytes = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+        // 32 channels of one entry with two scales into a tile
+        auto store = [&](uint8_t* tile, int e, const uint4& c, uint32_t b2) {
+            const uint32_t s2 = e4m3x2_to_h2(b2);
+            const uint32_t s_lo = __byte_perm(s2, 0u, 0x1010), s_hi = __byte_perm(s2, 0u, 0x3232);
+            uint8_t* dst = tile + (size_t)(qt >> 1) * DP_HALF + e * 128;
+            const bool rot = qt >> 1;  // the two quarters of a half store in another order: other banks
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int wi = rot ? (i + 2) & 3 : i;
+                const uint32_t sc = (rot ? ((i + 2) & 3) >> 1 : i >> 1) ? s_hi : s_lo;
+                uint32_t h0, h1, h2, h3;
+                e2m1x8_to_h2x4(rot ? word(c, (i + 2) & 3) : word(c, i), h0, h1, h2, h3);
+                *reinterpret_cast<uint4*>(dst + ((((qt & 1) * 4 + wi) ^ (e & 7)) << 4)) =
+                    make_uint4(hmul2(h0, sc), hmul2(h1, sc), hmul2(h2, sc), hmul2(h3, sc));
+            }
+        };
+        uint32_t n = 0;  // tiles so far
+        Row R[2];
+        uint32_t missing;
+        fetch(lo, R, missing);
+        for (uint32_t t = lo; t < hi; ++t, ++n) {
+            const int s = (int)(n & 1u);
+            if (n >= 2) wait(&kempty[s], ((n >> 1) - 1) & 1u);
+            uint8_t* kt = smem + DP_OFF_K + (size_t)s * DP_TILE;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t ks = word(R[i].s, qt >> 1) >> (16 * (qt & 1)) & 0xffffu;
+                // A NaN scale of V may not meet a weight of 0 in the product: V becomes 0 there
+                // and K NaN, so the tokens that see the entry get NaN and no other
+                const bool poison = qt == 0 && (nan_bytes(R[i].s.z) | nan_bytes(R[i].s.w));
+                store(kt, e0 + 64 * i, R[i].k, poison ? 0x7f7fu : ks);
+            }
+            // which entries are there, one bit each (lane 4 x: entry x of the warp's eight)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t m = __ballot_sync(0xffffffffu, !((missing >> i) & 1u)) & 0x11111111u;
+                m = (m | m >> 3) & 0x03030303u;
+                m = (m | m >> 6) & 0x000f000fu;
+                m = (m | m >> 12) & 0xffu;
+                if (lane == 0) smem[DP_OFF_OK + (n & 3u) * 16 + 8 * i + cw] = (uint8_t)m;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kfull[s]);
+            uint4 vcode[2];
+            uint32_t vscale[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                vcode[i] = R[i].v;
+                uint32_t b2 = word(R[i].s, 2 + (qt >> 1)) >> (16 * (qt & 1)) & 0xffffu;
+                if ((b2 & 0x7fu) == 0x7fu) b2 &= 0xff00u;
+                if ((b2 & 0x7f00u) == 0x7f00u) b2 &= 0x00ffu;
+                vscale[i] = b2;
+            }
+            if (t + 1 < hi) {  // the next tile's rows, in flight while V is converted
+                if (t + 1 >= w.t1) w.next(a);
+                fetch(t + 1, R, missing);
+            }
+            if (n >= 2) wait(&vempty[s], ((n >> 1) - 1) & 1u);
+            uint8_t* vt = smem + DP_OFF_V + (size_t)s * DP_TILE;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) store(vt, e0 + 64 * i, vcode[i], vscale[i]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vfull[s]);
+        }
+    } else if (lo < hi) {
+        // ================= softmax and results: row r of row tile i =================
+        const int i = wid >> 2, r = (wid & 3) * 32 + lane;
+        const uint32_t tS = tmem + ((uint32_t)((wid & 3) * 32) << 16) + 128u * i, tO = tS + 256u;
+        Walk w;
+        w.start(a, misc + 2);
+        uint32_t sn = 0, units = 0, n = 0;  // S tiles and units of this row tile, tiles of the CTA
+        if (tid == 0) {
+            d.cut[2 * blockIdx.x] = lo > w.t0 ? make_int4(w.s.row0 + w.k * DP_TOK, w.tokens(), (int)w.t0, (int)w.t1)
+                                              : make_int4(-1, 0, 0, 0);
+            d.cut[2 * blockIdx.x + 1] = make_int4((int)lo, 0, 0, 0);
+        }
+        for (uint32_t t = lo; t < hi;) {
+            const uint32_t first = t, end = min(hi, w.t1);
+            const int ntok = w.tokens(), tok = 8 * i + (r >> 4);
+            if (8 * i < ntok) {
+                const bool real = tok < ntok;
+                const int64_t row = ((int64_t)w.s.row0 + w.k * DP_TOK + tok) * kH + (r & 15);
+                const int seen = real ? seen_by(a, w.s, w.k * DP_TOK + tok) : 0;
+                // ---- Q: this row, scaled to fp16 ----------------------------------------------
+                float c = 1.f;
+                {
+                    const uint4* q = reinterpret_cast<const uint4*>(a.q + row * kD);
+                    float f = 0.f, am = 0.f;
+                    if (real) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint4 v[4] = {__ldg(q + 4 * x), __ldg(q + 4 * x + 1), __ldg(q + 4 * x + 2), __ldg(q + 4 * x + 3)};
+                            am = fmaxf(am, q_absmax(v));
+                        }
+                    }
+                    q_scale(am, f, c);
+                    uint8_t* dst = smem + DP_OFF_Q + (size_t)i * DP_TILE + r * 128;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const uint4 v = real ? __ldg(q + x) : make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(dst + (size_t)(x >> 3) * DP_HALF + (((x & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(q_half2(v.x, f), q_half2(v.y, f), q_half2(v.z, f), q_half2(v.w, f));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&qfull[i]);
+                }
+                float m = -INFINITY, bias = kPBias, l = 0.f;
+                for (; t < end; ++t, ++n, ++sn) {
+                    wait(&sfull[i], sn & 1u);
+                    tc_fence_after();
+                    const int nv = seen - (int)(t - w.t0) * DP_KEYS;  // entries of the tile this row sees
+                    const uint4 ok = *reinterpret_cast<const uint4*>(smem + DP_OFF_OK + (n & 3u) * 16);
+                    const bool all = __all_sync(0xffffffffu, nv >= DP_KEYS && (ok.x & ok.y & ok.z & ok.w) == ~0u);
+                    // the columns of chunk x that this row sees, one bit each
+                    auto cols = [&](int x) -> uint32_t {
+                        const int k = nv - 32 * x;
+                        const uint32_t b = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
+                        return b & (x == 0 ? ok.x : x == 1 ? ok.y : x == 2 ? ok.z : ok.w);
+                    };
+                    // ---- the row's maximum -----------------------------------------------------------
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t v[32];
+                        tmem_ld32(tS + 32u * x, v);
+                        tmem_wait_ld();
+                        if (!all) {
+                            const uint32_t b = cols(x);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((b >> e) & 1u)) v[e] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            mx = fmaxf(fmaxf(mx, __uint_as_float(v[e])), __uint_as_float(v[e + 1]));
+                    }
+                    mx *= c;  // log2 domain
+                    const bool rise = mx > -INFINITY && (m == -INFINITY || mx + bias > kPMax);
+                    if (__any_sync(0xffffffffu, rise)) {
+                        const float f = rise && m != -INFINITY ? ex2(m - mx) : 1.f;
+                        if (rise) {
+                            m = mx;
+                            bias = kPBias - mx;
+                            l *= f;
+                        }
+                        __syncwarp();
+                        if (t > first) {  // O is complete: S of this tile was issued after its last product
+#pragma unroll 1
+                            for (int x = 0; x < 4; ++x) {
+                                uint32_t v[32];
+                                tmem_ld32(tO + 32u * x, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                                tmem_st32(tO + 32u * x, v);
+                            }
+                        }
+                    }
+                    // ---- P over S, the sum -------------------------------------------------------------
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t v[32], p[16], q[16];
+                        tmem_ld32(tS + 32u * x, v);
+                        tmem_wait_ld();
+                        const uint32_t b = all ? ~0u : cols(x);
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float p0 = ex2(fmaf(__uint_as_float(v[e]), c, bias));
+                            float p1 = ex2(fmaf(__uint_as_float(v[e + 1]), c, bias));
+                            if (!all) {
+                                if (!((b >> e) & 1u)) p0 = 0.f;
+                                if (!((b >> e) & 2u)) p1 = 0.f;
+                            }
+                            s0 += p0;
+                            s1 += p1;
+                            p[e >> 1] = f2_to_h2(p0, p1);
+                            if (SPLIT) q[e >> 1] = rest_h2(p0, p1, p[e >> 1]);
+                        }
+                        l += s0 + s1;
+                        tmem_st16(tS + 32u * x, p);
+                        if (SPLIT) tmem_st16(tS + 32u * x + 16u, q);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[i]);
+                }
+                // ---- the unit's rows ---------------------------------------------------------------
+                wait(&ofull[i], units & 1u);
+                ++units;
+                tc_fence_after();
+                const bool whole = first == w.t0 && end == w.t1;
+                const int64_t part = (2 * (int64_t)blockIdx.x + (first == w.t0 ? 1 : 0)) * DP_ROWS + 128 * i + r;
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t v[32];
+                    tmem_ld32(tO + 32u * x, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32 && real; e += 8) {
+                        float o[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) o[y] = __uint_as_float(v[e + y]);
+                        if (whole) {
+                            dense_store(a, row, 32 * x + e, o, m, l);
+                        } else {
+                            float4* po = reinterpret_cast<float4*>(d.part_o + part * kD + 32 * x + e);
+                            po[0] = make_float4(o[0], o[1], o[2], o[3]);
+                            po[1] = make_float4(o[4], o[5], o[6], o[7]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!whole && real) {
+                    d.part_m[part] = m;
+                    d.part_l[part] = l;
+                }
+                tc_fence_before();
+            } else {
+                n += end - t;
+                t = end;
+            }
+            if (t < hi) w.next(a);
+        }
+    } else if (tid == 0) {
+        d.cut[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+    tc_fence_before();
+    __syncthreads();  // every accumulator has been read
+    if (wid == DP_W_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+    if (tid == 0 && *s_timeout) dev_error(a.err, CSA2_DEV_TIMEOUT);
+}
+
+// Joins the partial results of every unit that spans CTAs: block (c, y) token y
+// of the unit that CTA c continues, if CTA c - 1 began it; one warp per head,
+// sums in a fixed order.
+constexpr int DPJ_THREADS = kH * 32;
+__global__ void __launch_bounds__(DPJ_THREADS) dense_prefill_join_kernel(const PrefillDenseArgs d) {
+    const int c = blockIdx.x + 1, h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    const int4 cut = d.cut[2 * c];
+    if (cut.x < 0 || (int)blockIdx.y >= cut.y) return;
+    const int per = d.cut[2 * c + 1].x / c;   // CTA c begins at tile c * per
+    if (cut.z < (c - 1) * per) return;        // an earlier CTA's block does it
+    const int n = (cut.w - 1) / per - c + 2;  // parts
+    const int r = blockIdx.y * kH + h;
+    auto part = [&](int k) { return (int64_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * DP_ROWS + r; };
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, d.part_m[part(k)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+        const int64_t p = part(k);
+        const float m = d.part_m[p];
+        const float4 v = *reinterpret_cast<const float4*>(d.part_o + p * kD + 4 * lane);
+        const float f = m == -INFINITY ? 0.f : ex2(m - M);
+        o.x += v.x * f;
+        o.y += v.y * f;
+        o.z += v.z * f;
+        o.w += v.w * f;
+        l += d.part_l[p] * f;
+    }
+    // eight dims per storing lane
+    const float4 u = make_float4(__shfl_down_sync(0xffffffffu, o.x, 1), __shfl_down_sync(0xffffffffu, o.y, 1),
+                                 __shfl_down_sync(0xffffffffu, o.z, 1), __shfl_down_sync(0xffffffffu, o.w, 1));
+    if (!(lane & 1)) {
+        const float x[8] = {o.x, o.y, o.z, o.w, u.x, u.y, u.z, u.w};
+        dense_store(d.a, ((int64_t)cut.x + blockIdx.y) * kH + h, 4 * lane, x, M, l);
+    }
+}
+
+size_t dense_prefill_ws_bytes() {
+    return (size_t)2 * kDenseCtas * DP_ROWS * (kD + 2) * 4 + (size_t)2 * kDenseCtas * sizeof(int4);
+}
+
+cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stream) {
+    static bool init[64];
+    static int n_sm[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!init[dev]) {
+        for (const void* k : {(const void*)dense_prefill_kernel<false>, (const void*)dense_prefill_kernel<true>}) {
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DP_SMEM);
+            if (e != cudaSuccess) return e;
+        }
+        e = cudaDeviceGetAttribute(&n_sm[dev], cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        init[dev] = true;
+    }
+    PrefillDenseArgs d{};
+    d.a = a;
+    d.part_o = reinterpret_cast<float*>(ws);
+    d.part_m = d.part_o + (size_t)2 * kDenseCtas * DP_ROWS * kD;
+    d.part_l = d.part_m + (size_t)2 * kDenseCtas * DP_ROWS;
+    d.cut = reinterpret_cast<int4*>(d.part_l + (size_t)2 * kDenseCtas * DP_ROWS);
+    // tiles there can be: units times the longest sequence's tiles
+    const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS);
+    const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);
+    LaunchCfg c(dim3(ctas), dim3(DP_THREADS), DP_SMEM, stream);
+    e = a.out_bf16 ? cudaLaunchKernelEx(&c.cfg, dense_prefill_kernel<false>, (const PrefillDenseArgs)d)
+                   : cudaLaunchKernelEx(&c.cfg, dense_prefill_kernel<true>, (const PrefillDenseArgs)d);
+    if (e != cudaSuccess || ctas == 1) return e;
+    LaunchCfg j(dim3(ctas - 1, DP_TOK), dim3(DPJ_THREADS), 0, stream);
+    return cudaLaunchKernelEx(&j.cfg, dense_prefill_join_kernel, (const PrefillDenseArgs)d);
+}
+
+}  // namespace csa2

@@ -125,7 +125,7 @@ struct StageArgs {
 };
 cudaError_t launch_stage_rows(const StageArgs& a, int B, cudaStream_t stream);
 
-// Dense attention over every entry of the main KV (dense_attn.cu).
+// Dense attention over every entry of the main KV (checks: dense_attn.cu).
 struct DenseArgs {
     csa2_kv_cache cache;
     const uint16_t* q;        // [rows][16][128] bf16
@@ -138,9 +138,11 @@ struct DenseArgs {
     int32_t B, T, max_len, ratio, page_shift;
     bool out_bf16;
 };
-cudaError_t launch_dense_attn(const DenseArgs& a, char* ws, cudaStream_t stream);
 // One token per sequence (dense_decode.cu).
 size_t dense_decode_ws_bytes();
 cudaError_t launch_dense_decode(const DenseArgs& a, char* ws, cudaStream_t stream);
+// Ragged chunks of tokens (dense_prefill.cu).
+size_t dense_prefill_ws_bytes();
+cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stream);
 
 }  // namespace csa2

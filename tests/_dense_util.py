@@ -69,7 +69,10 @@ def reference(q, rows, seen, hidden=None):
     exp moves by ds relative, its own error is below 2^-20, the sum of n weights
     n * 2^-24; numerator and denominator each, so
       out: 2 (ds + 2^-20 + n 2^-24) sum w |v|   lse: ds + 2^-20 + n 2^-24 + 2^-23 |lse|
-    and the weights' rounding (the caller's) comes on top."""
+    and the weights' rounding (the caller's) comes on top.  Weights are held as
+    fp16 times 2^7 over a maximum that is at most the largest score, so the
+    smallest fp16 step, 2^-24, rounds a weight far below the largest by up to
+    2^-25 / 2^7 = 2^-32 (of a sum that is at least 1): 2^-32 sum |v| more."""
     n, L = q.shape[0], rows.shape[0]
     out = torch.zeros((n, 16, 128), dtype=torch.float64)
     lse = torch.full((n, 16), -math.inf, dtype=torch.float64)
@@ -91,7 +94,7 @@ def reference(q, rows, seen, hidden=None):
         spread[i] = w @ v.abs()
         ds = (mag * 128 * 2.0 ** -24 + s.abs() * 2.0 ** -22).amax(1)
         e = ds + 2.0 ** -20 + k.shape[0] * 2.0 ** -24
-        b_out[i] = 2 * e[:, None] * spread[i]
+        b_out[i] = 2 * e[:, None] * spread[i] + v.abs().sum(0) * 2.0 ** -32
         b_lse[i] = e + lse[i].abs() * 2.0 ** -23
     return out, lse, spread, b_out, b_lse
 
