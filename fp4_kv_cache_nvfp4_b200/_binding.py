@@ -115,10 +115,11 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
+    """The raw handle of a stream; of the current device's current stream for None."""
     if stream is None:
-        if not torch.cuda.is_available():
-            return None
-        stream = torch.cuda.current_stream()
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -147,10 +148,16 @@ def _tensor(name: str, t, dtypes, shape, optional: bool = False) -> None:
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
-def _on_gpu(name: str, t, dtypes, shape, optional: bool = False) -> None:
-    _tensor(name, t, dtypes, shape, optional)
-    if t is not None and not t.is_cuda:
-        raise ValueError(f"{name}: on {t.device}, expected the GPU")
+def _on_gpu(name: str, t, dtypes, shape, dev: int, optional: bool = False) -> None:
+    """_tensor, and on GPU `dev`: one quick look where all is well (a decode call
+    makes half a dozen of these)."""
+    if t is None and optional:
+        return
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev and t.is_contiguous() and \
+            (t.shape == shape or (shape[-1] is None and t.dim() == len(shape))):
+        return
+    _tensor(name, t, dtypes, shape)
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
 
 
 def abi_version() -> int:
@@ -325,15 +332,30 @@ def dense_attn_workspace_bytes(desc: LayerDesc, B: int, prefill: bool = False) -
     return int(lib().csa2_dense_attn_workspace_bytes(ctypes.byref(desc), B, 1 if prefill else 0))
 
 
-def _dense_checks(q, seq_lens, out, lse, workspace, err, B: int) -> int:
-    T = q.shape[0]
-    _on_gpu("q", q, _BITS16, (T, 16, 128))
-    _on_gpu("seq_lens", seq_lens, (torch.int32,), (B,))
-    _on_gpu("out", out, tuple(_OUT), (T, 16, 128))
-    _on_gpu("lse", lse, (torch.float32,), (T, 16))
-    _on_gpu("workspace", workspace, (torch.uint8,), (None,))
-    _on_gpu("err", err, (torch.int32,), (1,), optional=True)
-    return _OUT[out.dtype]
+_I32T, _U8T, _F32T, _OUTT = (torch.int32,), (torch.uint8,), (torch.float32,), (torch.float32, torch.bfloat16)
+
+
+def _device(t) -> int:
+    """The current GPU, where the call's tensors have to be (t decides nothing: it
+    only keeps a CPU tensor from initialising CUDA)."""
+    if isinstance(t, torch.Tensor) and not t.is_cuda:
+        raise ValueError(f"a tensor on {t.device}, expected the GPU")
+    return torch.cuda.current_device()
+
+
+def _dense_checks(cache: KVCache, q, seq_lens, out, lse, workspace, err, B: int) -> tuple[int, int]:
+    dev, T = _device(q), q.shape[0]
+    _on_gpu("q", q, _BITS16, (T, 16, 128), dev)
+    _on_gpu("seq_lens", seq_lens, _I32T, (B,), dev)
+    _on_gpu("out", out, _OUTT, (T, 16, 128), dev)
+    _on_gpu("lse", lse, _F32T, (T, 16), dev)
+    _on_gpu("workspace", workspace, _U8T, (None,), dev)
+    _on_gpu("err", err, _I32T, (1,), dev, optional=True)
+    if cache.page_table.shape[0] < B:
+        raise ValueError(f"seq_lens: {B} sequences, the page table has {cache.page_table.shape[0]}")
+    if cache.page_table.get_device() != dev:
+        raise ValueError(f"cache: on {cache.page_table.device}, expected cuda:{dev}")
+    return _OUT[out.dtype], dev
 
 
 def dense_attn_decode(desc: LayerDesc, cache: KVCache, q, seq_lens, out, lse, max_len: int, workspace: torch.Tensor,
@@ -341,14 +363,12 @@ def dense_attn_decode(desc: LayerDesc, cache: KVCache, q, seq_lens, out, lse, ma
     """One token per sequence (q [B, 16, 128] bf16) over every entry of its
     sequence; out fp32 or bf16, lse fp32 [B, 16]."""
     B = seq_lens.numel()
-    dt = _dense_checks(q, seq_lens, out, lse, workspace, err, B)
+    dt, _ = _dense_checks(cache, q, seq_lens, out, lse, workspace, err, B)
     if q.shape[0] != B:
         raise ValueError(f"q: {q.shape[0]} rows for {B} sequences")
-    if cache.page_table.shape[0] < B:
-        raise ValueError(f"seq_lens: {B} sequences, the page table has {cache.page_table.shape[0]}")
-    _check(lib().csa2_dense_attn_decode(ctypes.byref(desc), ctypes.byref(cache.struct()), _ptr(q), _ptr(seq_lens),
-                                        _ptr(out), dt, _ptr(lse), B, max_len, _ptr(workspace), workspace.numel(),
-                                        _ptr(err), _stream(stream)), "dense_attn_decode")
+    _check(lib().csa2_dense_attn_decode(ctypes.byref(desc), ctypes.byref(cache._s), q.data_ptr(), seq_lens.data_ptr(),
+                                        out.data_ptr(), dt, lse.data_ptr(), B, max_len, workspace.data_ptr(),
+                                        workspace.numel(), _ptr(err), _stream(stream)), "dense_attn_decode")
 
 
 def dense_attn_prefill(desc: LayerDesc, cache: KVCache, q, cu_q, seq_lens, out, lse, max_len: int,
@@ -357,15 +377,13 @@ def dense_attn_prefill(desc: LayerDesc, cache: KVCache, q, cu_q, seq_lens, out, 
     over their sequence's entries: causal from position q_start[b] on (desc.ratio
     tokens per entry), or over every entry without q_start."""
     B = seq_lens.numel()
-    dt = _dense_checks(q, seq_lens, out, lse, workspace, err, B)
-    _on_gpu("cu_q", cu_q, (torch.int32,), (B + 1,))
-    _on_gpu("q_start", q_start, (torch.int32,), (B,), optional=True)
-    if cache.page_table.shape[0] < B:
-        raise ValueError(f"seq_lens: {B} sequences, the page table has {cache.page_table.shape[0]}")
-    _check(lib().csa2_dense_attn_prefill(ctypes.byref(desc), ctypes.byref(cache.struct()), _ptr(q), _ptr(cu_q),
-                                         _ptr(q_start), _ptr(seq_lens), _ptr(out), dt, _ptr(lse), B, q.shape[0],
-                                         max_len, _ptr(workspace), workspace.numel(), _ptr(err), _stream(stream)),
-           "dense_attn_prefill")
+    dt, dev = _dense_checks(cache, q, seq_lens, out, lse, workspace, err, B)
+    _on_gpu("cu_q", cu_q, _I32T, (B + 1,), dev)
+    _on_gpu("q_start", q_start, _I32T, (B,), dev, optional=True)
+    _check(lib().csa2_dense_attn_prefill(ctypes.byref(desc), ctypes.byref(cache._s), q.data_ptr(), cu_q.data_ptr(),
+                                         _ptr(q_start), seq_lens.data_ptr(), out.data_ptr(), dt, lse.data_ptr(), B,
+                                         q.shape[0], max_len, workspace.data_ptr(), workspace.numel(), _ptr(err),
+                                         _stream(stream)), "dense_attn_prefill")
 
 
 def kv_pages_workspace_bytes(n_phys_pages: int, n: int = 0) -> int:
@@ -377,28 +395,31 @@ def kv_pages_workspace_bytes(n_phys_pages: int, n: int = 0) -> int:
 
 
 def _page_args(caches, refs, seq_lens, err):
-    """The caches as a C array, and their common table."""
+    """The caches as a C array, their common table and the device."""
     if not caches:
         raise ValueError("caches: empty")
     c0 = caches[0]
+    table = c0.page_table
+    dev = _device(table)
     for c in caches[1:]:
-        if c.page_table.data_ptr() != c0.page_table.data_ptr() or c.page_table.shape != c0.page_table.shape:
+        if c.page_table.data_ptr() != table.data_ptr() or c.page_table.shape != table.shape:
             raise ValueError("caches: they do not share one page table")
-    _on_gpu("page_table", c0.page_table, (torch.int32,), (None, None))
-    _on_gpu("refs", refs, (torch.int32,), (c0.n_phys_pages,))
-    _on_gpu("seq_lens", seq_lens, (torch.int32,), (c0.page_table.shape[0],), optional=True)
-    _on_gpu("err", err, (torch.int32,), (1,), optional=True)
-    return (_Cache * len(caches))(*[c.struct() for c in caches]), c0.page_table
+    _on_gpu("page_table", table, _I32T, tuple(table.shape), dev)
+    _on_gpu("refs", refs, _I32T, (c0.n_phys_pages,), dev)
+    _on_gpu("seq_lens", seq_lens, _I32T, (table.shape[0],), dev, optional=True)
+    _on_gpu("err", err, _I32T, (1,), dev, optional=True)
+    return ctypes.byref(c0._s) if len(caches) == 1 else (_Cache * len(caches))(*[c._s for c in caches]), table, dev
 
 
 def kv_pages_copy(caches: list[KVCache], src, dst, err=None, stream=None) -> None:
     """Physical pages src[i] -> dst[i] in every cache (int32; a -1 skips the pair)."""
-    _on_gpu("src", src, (torch.int32,), (None,))
-    _on_gpu("dst", dst, (torch.int32,), (src.numel(),))
-    _on_gpu("err", err, (torch.int32,), (1,), optional=True)
     if not caches:
         raise ValueError("caches: empty")
-    C = (_Cache * len(caches))(*[c.struct() for c in caches])
+    dev = _device(src)
+    _on_gpu("src", src, _I32T, (None,), dev)
+    _on_gpu("dst", dst, _I32T, (src.numel(),), dev)
+    _on_gpu("err", err, _I32T, (1,), dev, optional=True)
+    C = (_Cache * len(caches))(*[c._s for c in caches])
     _check(lib().csa2_kv_pages_copy(len(caches), C, _ptr(src), _ptr(dst), src.numel(), _ptr(err), _stream(stream)),
            "kv_pages_copy")
 
@@ -406,10 +427,10 @@ def kv_pages_copy(caches: list[KVCache], src, dst, err=None, stream=None) -> Non
 def kv_pages_fork(caches: list[KVCache], refs, seq_lens, parents, children, workspace: torch.Tensor, err=None,
                   stream=None) -> None:
     """Rows children[i] of the caches' page table share what rows parents[i] hold."""
-    C, table = _page_args(caches, refs, seq_lens, err)
-    _on_gpu("parents", parents, (torch.int32,), (None,))
-    _on_gpu("children", children, (torch.int32,), (parents.numel(),))
-    _on_gpu("workspace", workspace, (torch.uint8,), (None,))
+    C, table, dev = _page_args(caches, refs, seq_lens, err)
+    _on_gpu("parents", parents, _I32T, (None,), dev)
+    _on_gpu("children", children, _I32T, (parents.numel(),), dev)
+    _on_gpu("workspace", workspace, _U8T, (None,), dev)
     _check(lib().csa2_kv_pages_fork(len(caches), C, _ptr(table), table.shape[0], _ptr(refs), _ptr(seq_lens),
                                     _ptr(parents), _ptr(children), parents.numel(), _ptr(workspace),
                                     workspace.numel(), _ptr(err), _stream(stream)), "kv_pages_fork")
@@ -417,8 +438,8 @@ def kv_pages_fork(caches: list[KVCache], refs, seq_lens, parents, children, work
 
 def kv_pages_free(cache: KVCache, refs, seq_lens, seqs, err=None, stream=None) -> None:
     """Rows seqs[i] of the page table become free; their pages lose one holder each."""
-    C, table = _page_args([cache], refs, seq_lens, err)
-    _on_gpu("seqs", seqs, (torch.int32,), (None,))
+    C, table, dev = _page_args([cache], refs, seq_lens, err)
+    _on_gpu("seqs", seqs, _I32T, (None,), dev)
     _check(lib().csa2_kv_pages_free(C, _ptr(table), table.shape[0], _ptr(refs), _ptr(seq_lens), _ptr(seqs),
                                     seqs.numel(), _ptr(err), _stream(stream)), "kv_pages_free")
 
@@ -428,10 +449,10 @@ def kv_pages_compact(caches: list[KVCache], refs, page_map, n_live, workspace: t
     """Live pages move into the free numbers below their count; the page table and
     refs follow, page_map [n_phys_pages] tells each page's new number (-1: free)
     and n_live [1] their count."""
-    C, table = _page_args(caches, refs, None, err)
-    _on_gpu("page_map", page_map, (torch.int32,), (caches[0].n_phys_pages,))
-    _on_gpu("n_live", n_live, (torch.int32,), (1,))
-    _on_gpu("workspace", workspace, (torch.uint8,), (None,))
+    C, table, dev = _page_args(caches, refs, None, err)
+    _on_gpu("page_map", page_map, _I32T, (caches[0].n_phys_pages,), dev)
+    _on_gpu("n_live", n_live, _I32T, (1,), dev)
+    _on_gpu("workspace", workspace, _U8T, (None,), dev)
     _check(lib().csa2_kv_pages_compact(len(caches), C, _ptr(table), table.shape[0], _ptr(refs), _ptr(page_map),
                                        _ptr(n_live), _ptr(workspace), workspace.numel(), _ptr(err), _stream(stream)),
            "kv_pages_compact")

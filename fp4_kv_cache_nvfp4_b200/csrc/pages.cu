@@ -24,6 +24,10 @@ constexpr int kMaxPages = 1 << 22;      // physical pages of a cache
 constexpr int PG_CHUNK = 4096;          // reference counts per CTA
 constexpr int PG_SCAN_THREADS = 1024;   // four counts per thread
 constexpr int PG_COPY_THREADS = 256;
+// Up to this many chunks every CTA counts the chunks before its own (and, to
+// compact, all) itself from L2; above, a kernel counts each chunk once first.
+// COUNTS_MEASURED
+constexpr int PG_SELF_COUNT = 16;
 
 struct PageCaches {
     uint8_t* codes[kMaxCaches];
@@ -108,19 +112,48 @@ struct ForkArgs {
     int32_t n, n_seqs, max_pages, n_pages, page_shift;
 };
 
-// CTAs 0 .. chunks-1 count the free pages of their chunk; the last CTA checks
-// the requests and ranks those that need a page.
+__device__ __forceinline__ uint32_t free_of(const int4& v) {
+    return (uint32_t)(v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+}
+
+// Free pages of each chunk.
 __global__ void __launch_bounds__(PG_SCAN_THREADS) fork_count_kernel(ForkArgs a) {
     __shared__ uint32_t tmp[64];
-    __shared__ int32_t s_child[kMaxForks], s_parent[kMaxForks];
-    const int tid = threadIdx.x;
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x + 1 < gridDim.x) {
-        const int4 v = load_refs(a.refs, a.n_pages, (int)blockIdx.x * PG_CHUNK + 4 * tid);
-        uint32_t total;
-        block_excl_scan((uint32_t)(v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0), tmp, &total);
-        if (tid == 0) a.chunk_free[blockIdx.x] = (int)total;
+    uint32_t total;
+    block_excl_scan(free_of(load_refs(a.refs, a.n_pages, (int)blockIdx.x * PG_CHUNK + 4 * (int)threadIdx.x)), tmp, &total);
+    if (threadIdx.x == 0) a.chunk_free[blockIdx.x] = (int)total;
+}
+
+// CTAs 0 .. chunks-1 list the first n free pages, ascending; the last CTA checks
+// the requests and ranks those that need a page.
+__global__ void __launch_bounds__(PG_SCAN_THREADS) fork_list_kernel(ForkArgs a) {
+    __shared__ uint32_t tmp[64];
+    __shared__ int32_t s_child[kMaxForks], s_parent[kMaxForks];
+    const int tid = threadIdx.x, chunks = (int)gridDim.x - 1;
+    pdl_wait();
+    pdl_trigger();
+    if ((int)blockIdx.x < chunks) {
+        uint32_t mine = 0;
+        if (chunks <= PG_SELF_COUNT) {
+            for (int c = 0; c < (int)blockIdx.x; ++c) mine += free_of(load_refs(a.refs, a.n_pages, c * PG_CHUNK + 4 * tid));
+        } else {
+            for (int c = tid; c < (int)blockIdx.x; c += PG_SCAN_THREADS) mine += (uint32_t)a.chunk_free[c];
+        }
+        uint32_t before, total;
+        block_excl_scan(mine, tmp, &before);  // the scan's total
+        const int at = (int)blockIdx.x * PG_CHUNK + 4 * tid;
+        const int4 v = load_refs(a.refs, a.n_pages, at);
+        const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
+        uint32_t r = before + block_excl_scan((uint32_t)(f[0] + f[1] + f[2] + f[3]), tmp, &total);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (f[e]) {
+                if (r < (uint32_t)a.n) a.free_list[r] = at + e;
+                ++r;
+            }
+        if ((int)blockIdx.x + 1 == chunks && tid == 0) *a.n_free = (int)(before + total);
         return;
     }
     if (tid < a.n) {
@@ -165,30 +198,6 @@ __global__ void __launch_bounds__(PG_SCAN_THREADS) fork_count_kernel(ForkArgs a)
     const uint32_t rank = block_excl_scan(part ? 1u : 0u, tmp, &total);
     if (part) pl.rank = (int)rank;
     if (tid < a.n) a.plan[tid] = pl;
-}
-
-// The first n free pages, ascending.
-__global__ void __launch_bounds__(PG_SCAN_THREADS) fork_list_kernel(ForkArgs a) {
-    __shared__ uint32_t tmp[64];
-    const int tid = threadIdx.x;
-    pdl_wait();
-    pdl_trigger();
-    uint32_t mine = 0;
-    for (int c = tid; c < (int)blockIdx.x; c += PG_SCAN_THREADS) mine += (uint32_t)a.chunk_free[c];
-    uint32_t before;
-    block_excl_scan(mine, tmp, &before);
-    const int at = (int)blockIdx.x * PG_CHUNK + 4 * tid;
-    const int4 v = load_refs(a.refs, a.n_pages, at);
-    const int f[4] = {v.x == 0, v.y == 0, v.z == 0, v.w == 0};
-    uint32_t total;
-    uint32_t r = before + block_excl_scan((uint32_t)(f[0] + f[1] + f[2] + f[3]), tmp, &total);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (f[e]) {
-            if (r < (uint32_t)a.n) a.free_list[r] = at + e;
-            ++r;
-        }
-    if (blockIdx.x + 1 == gridDim.x && tid == 0) *a.n_free = (int)(before + total);
 }
 
 // CTA (i, 0) fills child i's row and counts its pages; CTA (i, 1 + c) copies
@@ -280,31 +289,42 @@ struct CompactArgs {
 };
 
 // Live pages (count > 0) of each chunk of PG_CHUNK.
+__device__ __forceinline__ uint32_t live_in(const int32_t* refs, int n_pages, int at, int below) {
+    const int4 v = load_refs(refs, n_pages, at);
+    const int end = min(n_pages, below);
+    return (uint32_t)(v.x > 0 && at < end) + (v.y > 0 && at + 1 < end) + (v.z > 0 && at + 2 < end) +
+           (v.w > 0 && at + 3 < end);
+}
 __global__ void __launch_bounds__(PG_SCAN_THREADS) compact_count_kernel(CompactArgs a) {
     __shared__ uint32_t tmp[64];
-    const int tid = threadIdx.x, at = (int)blockIdx.x * PG_CHUNK + 4 * tid;
     pdl_wait();
     pdl_trigger();
-    const int4 v = load_refs(a.refs, a.n_pages, at);
-    const uint32_t c = (uint32_t)(v.x > 0 && at < a.n_pages) + (v.y > 0 && at + 1 < a.n_pages) +
-                       (v.z > 0 && at + 2 < a.n_pages) + (v.w > 0 && at + 3 < a.n_pages);
     uint32_t total;
-    block_excl_scan(c, tmp, &total);
-    if (tid == 0) a.chunk_live[blockIdx.x] = (int)total;
+    block_excl_scan(live_in(a.refs, a.n_pages, (int)blockIdx.x * PG_CHUNK + 4 * (int)threadIdx.x, a.n_pages), tmp, &total);
+    if (threadIdx.x == 0) a.chunk_live[blockIdx.x] = (int)total;
 }
 
-// Every CTA sums the chunks' counts (those before its own, all, and those
-// before n_live's), then ranks its pages.
+// Every CTA sums the live pages of all chunks, of those before its own and of
+// those below n_live, then ranks its pages.
 __global__ void __launch_bounds__(PG_SCAN_THREADS) compact_list_kernel(CompactArgs a) {
     __shared__ uint32_t tmp[64];
     const int tid = threadIdx.x, chunks = (int)gridDim.x, at = (int)blockIdx.x * PG_CHUNK + 4 * tid;
+    const bool self = chunks <= PG_SELF_COUNT;
     pdl_wait();
     pdl_trigger();
     uint32_t mine = 0, all = 0;
-    for (int c = tid; c < chunks; c += PG_SCAN_THREADS) {
-        const uint32_t x = (uint32_t)a.chunk_live[c];
-        all += x;
-        if (c < (int)blockIdx.x) mine += x;
+    if (self) {
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t x = live_in(a.refs, a.n_pages, c * PG_CHUNK + 4 * tid, a.n_pages);
+            all += x;
+            if (c < (int)blockIdx.x) mine += x;
+        }
+    } else {
+        for (int c = tid; c < chunks; c += PG_SCAN_THREADS) {
+            const uint32_t x = (uint32_t)a.chunk_live[c];
+            all += x;
+            if (c < (int)blockIdx.x) mine += x;
+        }
     }
     uint32_t before, n_live, low;
     block_excl_scan(mine, tmp, &before);
@@ -312,14 +332,11 @@ __global__ void __launch_bounds__(PG_SCAN_THREADS) compact_list_kernel(CompactAr
     // live pages below n_live: whole chunks, and the part of the chunk it falls into
     const int cut = (int)(n_live / PG_CHUNK);
     uint32_t l = 0;
-    for (int c = tid; c < cut; c += PG_SCAN_THREADS) l += (uint32_t)a.chunk_live[c];
-    {
-        const int ca = cut * PG_CHUNK + 4 * tid;
-        const int4 v = load_refs(a.refs, a.n_pages, ca);
-        const int r[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) l += (uint32_t)(ca + e < (int)n_live && r[e] > 0);
-    }
+    if (self)
+        for (int c = 0; c < cut; ++c) l += live_in(a.refs, a.n_pages, c * PG_CHUNK + 4 * tid, a.n_pages);
+    else
+        for (int c = tid; c < cut; c += PG_SCAN_THREADS) l += (uint32_t)a.chunk_live[c];
+    l += live_in(a.refs, a.n_pages, cut * PG_CHUNK + 4 * tid, (int)n_live);
     block_excl_scan(l, tmp, &low);
     const int4 v = load_refs(a.refs, a.n_pages, at);
     const int r[4] = {v.x, v.y, v.z, v.w};
@@ -496,8 +513,9 @@ csa2_status csa2_kv_pages_fork(int32_t n_caches, const csa2_kv_cache* caches, in
     a.page_shift = page_shift_of(caches[0]);
     const unsigned chunks = (unsigned)((n_pages + PG_CHUNK - 1) / PG_CHUNK);
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = go(fork_count_kernel, dim3(chunks + 1), PG_SCAN_THREADS, st, a);
-    if (e == cudaSuccess) e = go(fork_list_kernel, dim3(chunks), PG_SCAN_THREADS, st, a);
+    cudaError_t e = cudaSuccess;
+    if (chunks > PG_SELF_COUNT) e = go(fork_count_kernel, dim3(chunks), PG_SCAN_THREADS, st, a);
+    if (e == cudaSuccess) e = go(fork_list_kernel, dim3(chunks + 1), PG_SCAN_THREADS, st, a);
     if (e == cudaSuccess)
         e = go(fork_apply_kernel, dim3((unsigned)n, 1u + (unsigned)n_caches), PG_COPY_THREADS, st, a);
     return from_cuda(e);
@@ -541,7 +559,8 @@ csa2_status csa2_kv_pages_compact(int32_t n_caches, const csa2_kv_cache* caches,
     a.n_pages = (int32_t)n_pages;
     const unsigned chunks = (unsigned)((n_pages + PG_CHUNK - 1) / PG_CHUNK);
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = go(compact_count_kernel, dim3(chunks), PG_SCAN_THREADS, st, a);
+    cudaError_t e = cudaSuccess;
+    if (chunks > PG_SELF_COUNT) e = go(compact_count_kernel, dim3(chunks), PG_SCAN_THREADS, st, a);
     if (e == cudaSuccess) e = go(compact_list_kernel, dim3(chunks), PG_SCAN_THREADS, st, a);
     const int64_t jobs = std::max<int64_t>(n_pages / 2 * n_caches, (a.table_size + 1023) / 1024);
     if (e == cudaSuccess)
