@@ -14,9 +14,9 @@
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread per row: maximum,
 //                   P = 2^(S c - m) as fp16 back into TMEM over S, the sum;
 //                   O's rescaling when m rises (rare); the result's rows
-//   warps 8-15      K and V of the next tiles: FP4 read with plain loads one tile
+//   warps 8-11      K and V of the next tiles: FP4 read with plain loads one tile
 //                   ahead, dequantised to fp16 (exact) into swizzled shared tiles
-//   warp 16         issues the products: while one row tile is in its softmax, the
+//   warp 12         issues the products: while one row tile is in its softmax, the
 //                   other's products run
 // TMEM: S of both row tiles (P over them), O of both: all 512 columns.
 //
@@ -38,8 +38,10 @@ constexpr int DP_ROWS = DP_TOK * kH;             // 256
 constexpr int DP_KEYS = 128;                     // entries per tile
 constexpr uint32_t DP_HALF = 128 * 128;          // 64 channels of an operand tile: [128 rows][128 B], swizzled
 constexpr uint32_t DP_TILE = 2 * DP_HALF;        // 32 KiB
-constexpr int DP_W_CONV = 8, DP_NCONV = 8, DP_W_MMA = 16, DP_WARPS = 17;
+constexpr int DP_W_CONV = 8, DP_NCONV = 4, DP_W_MMA = 12, DP_WARPS = 13;  // four warps a scheduler at most: 128 registers a thread
 constexpr int DP_THREADS = DP_WARPS * 32;
+constexpr int DP_STEP = DP_NCONV * 8;            // a converter thread's entries are that far apart ...
+constexpr int DP_ENT = DP_KEYS / DP_STEP;        // ... and so many
 constexpr size_t DP_OFF_Q = 0;                            // [2 row tiles]
 constexpr size_t DP_OFF_K = DP_OFF_Q + 2 * DP_TILE;       // [2 slots]
 constexpr size_t DP_OFF_V = DP_OFF_K + 2 * DP_TILE;       // [2 slots]
@@ -189,6 +191,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]
         "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
         "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr)
         : "memory");
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -345,87 +365,107 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         __syncwarp();
     } else if (lo < hi && wid >= DP_W_CONV) {
         // ================= converters: FP4 rows -> fp16 operand tiles =================
-        // Thread ct owns quarter qt (32 channels of K and of V) of entries e0 and e0 + 64.
+        // Thread ct owns quarter qt (32 channels of K and of V) of entries e0 + DP_STEP i.
         const int ct = tid - DP_W_CONV * 32, qt = ct & 3, e0 = ct >> 2, cw = wid - DP_W_CONV;
+        // The two quarters of a 64-channel half write their four 16-byte pieces one
+        // after the other, the other half's begin with the third, so that eight lanes
+        // write to distinct banks; the codes are loaded in that order.
+        const int rot = qt >> 1;
+        uint32_t off[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            off[i] = (uint32_t)rot * DP_HALF + (uint32_t)e0 * 128u + ((((qt & 1) * 4 + ((i + 2 * rot) & 3)) ^ (e0 & 7)) << 4);
+        const uint32_t pick0 = rot ? 0x3232u : 0x1010u, pick1 = rot ? 0x1010u : 0x3232u;
         Walk w;
         w.start(a, misc + 2);
         struct Row {
-            uint4 k, v, s;  // codes of the quarter, the entry's 16 scales (zeros: not there)
+            uint2 k[2], v[2];  // codes of the quarter, in writing order (zeros: not there)
+            uint32_t ks, vs;   // its two scales
         };
-        auto fetch = [&](uint32_t t, Row (&R)[2], uint32_t& missing) {
+        auto fetch = [&](uint32_t t, Row (&R)[DP_ENT], uint32_t& missing) {
             missing = 0;
+            const int32_t* pages = a.cache.page_table + (int64_t)w.b * a.cache.max_pages_per_seq;
+            const int pos0 = (int)(t - w.t0) * DP_KEYS + e0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int pos = (int)(t - w.t0) * DP_KEYS + e0 + 64 * i;
-                R[i].k = R[i].v = R[i].s = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < DP_ENT; ++i) {
+                const int pos = pos0 + DP_STEP * i;
+                R[i].k[0] = R[i].k[1] = R[i].v[0] = R[i].v[1] = make_uint2(0, 0);
+                R[i].ks = R[i].vs = 0;
                 if (pos < w.s.len) {
-                    const int64_t slot = entry_slot(a.cache, a.page_shift, w.b, pos, a.err);
-                    if (slot >= 0) {
-                        const uint4* c = reinterpret_cast<const uint4*>(a.cache.codes + slot * kCodeBytes);
-                        R[i].k = __ldg(c + qt);
-                        R[i].v = __ldg(c + 4 + qt);
-                        R[i].s = __ldg(reinterpret_cast<const uint4*>(a.cache.scales + slot * kScales));
+                    const int32_t pg = __ldg(pages + (pos >> a.page_shift));
+                    if (pg >= 0 && pg < a.cache.n_phys_pages) {
+                        const int slot = (pg << a.page_shift) | (pos & ((1 << a.page_shift) - 1));
+                        const uint8_t* c = a.cache.codes + (int64_t)slot * kCodeBytes + 16 * qt;
+                        const uint8_t* s = a.cache.scales + (int64_t)slot * kScales + 2 * qt;
+                        R[i].k[0] = __ldg(reinterpret_cast<const uint2*>(c + 8 * rot));
+                        R[i].k[1] = __ldg(reinterpret_cast<const uint2*>(c + 8 * (rot ^ 1)));
+                        R[i].v[0] = __ldg(reinterpret_cast<const uint2*>(c + 64 + 8 * rot));
+                        R[i].v[1] = __ldg(reinterpret_cast<const uint2*>(c + 64 + 8 * (rot ^ 1)));
+                        R[i].ks = __ldg(reinterpret_cast<const uint16_t*>(s));
+                        R[i].vs = __ldg(reinterpret_cast<const uint16_t*>(s + 8));
                     } else {
+                        dev_error(a.err, CSA2_DEV_PAGE);
                         missing |= 1u << i;
                     }
                 }
             }
         };
-        auto word = [](const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
-        auto nan_bytes = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
         // 32 channels of one entry with two scales into a tile
-        auto store = [&](uint8_t* tile, int e, const uint4& c, uint32_t b2) {
-            const uint32_t s2 = e4m3x2_to_h2(b2);
-            const uint32_t s_lo = __byte_perm(s2, 0u, 0x1010), s_hi = __byte_perm(s2, 0u, 0x3232);
-            uint8_t* dst = tile + (size_t)(qt >> 1) * DP_HALF + e * 128;
-            const bool rot = qt >> 1;  // the two quarters of a half store in another order: other banks
+        auto store = [&](uint8_t* tile, const uint2 (&c)[2], uint32_t b2) {
+            const uint32_t s2 = e4m3x2_to_h2(b2), s0 = __byte_perm(s2, 0u, pick0), s1 = __byte_perm(s2, 0u, pick1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int wi = rot ? (i + 2) & 3 : i;
-                const uint32_t sc = (rot ? ((i + 2) & 3) >> 1 : i >> 1) ? s_hi : s_lo;
+                const uint32_t sc = i < 2 ? s0 : s1;
                 uint32_t h0, h1, h2, h3;
-                e2m1x8_to_h2x4(rot ? word(c, (i + 2) & 3) : word(c, i), h0, h1, h2, h3);
-                *reinterpret_cast<uint4*>(dst + ((((qt & 1) * 4 + wi) ^ (e & 7)) << 4)) =
-                    make_uint4(hmul2(h0, sc), hmul2(h1, sc), hmul2(h2, sc), hmul2(h3, sc));
+                e2m1x8_to_h2x4(i == 0 ? c[0].x : i == 1 ? c[0].y : i == 2 ? c[1].x : c[1].y, h0, h1, h2, h3);
+                *reinterpret_cast<uint4*>(tile + off[i]) = make_uint4(hmul2(h0, sc), hmul2(h1, sc), hmul2(h2, sc), hmul2(h3, sc));
             }
         };
         uint32_t n = 0;  // tiles so far
-        Row R[2];
+        Row R[DP_ENT];
         uint32_t missing;
         fetch(lo, R, missing);
         for (uint32_t t = lo; t < hi; ++t, ++n) {
             const int s = (int)(n & 1u);
+            // A NaN scale of V may not meet a weight of 0 in the product: V becomes 0 there
+            // and K NaN, so the tokens that see the entry get NaN and no other.
+            auto nan_pair = [](uint32_t x) { return ((x & 0x7f7fu) + 0x0101u) & 0x8080u; };
+            uint32_t nan = 0;
+#pragma unroll
+            for (int i = 0; i < DP_ENT; ++i) nan |= nan_pair(R[i].vs);
+            if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll
+                for (int i = 0; i < DP_ENT; ++i) {
+                    uint32_t x = nan_pair(R[i].vs);
+                    R[i].vs &= ~(x | (x - (x >> 7)));  // 0x80 of a byte -> 0xff
+                    x |= __shfl_xor_sync(0xffffffffu, x, 1);
+                    x |= __shfl_xor_sync(0xffffffffu, x, 2);
+                    if (x) R[i].ks = 0x7f7fu;
+                }
+            }
             if (n >= 2) wait(&kempty[s], ((n >> 1) - 1) & 1u);
             uint8_t* kt = smem + DP_OFF_K + (size_t)s * DP_TILE;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t ks = word(R[i].s, qt >> 1) >> (16 * (qt & 1)) & 0xffffu;
-                // A NaN scale of V may not meet a weight of 0 in the product: V becomes 0 there
-                // and K NaN, so the tokens that see the entry get NaN and no other
-                const bool poison = qt == 0 && (nan_bytes(R[i].s.z) | nan_bytes(R[i].s.w));
-                store(kt, e0 + 64 * i, R[i].k, poison ? 0x7f7fu : ks);
-            }
+            for (int i = 0; i < DP_ENT; ++i) store(kt + DP_STEP * 128 * i, R[i].k, R[i].ks);
             // which entries are there, one bit each (lane 4 x: entry x of the warp's eight)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < DP_ENT; ++i) {
                 uint32_t m = __ballot_sync(0xffffffffu, !((missing >> i) & 1u)) & 0x11111111u;
                 m = (m | m >> 3) & 0x03030303u;
                 m = (m | m >> 6) & 0x000f000fu;
                 m = (m | m >> 12) & 0xffu;
-                if (lane == 0) smem[DP_OFF_OK + (n & 3u) * 16 + 8 * i + cw] = (uint8_t)m;
+                if (lane == 0) smem[DP_OFF_OK + (n & 3u) * 16 + DP_STEP / 8 * i + cw] = (uint8_t)m;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&kfull[s]);
-            uint4 vcode[2];
-            uint32_t vscale[2];
+            uint2 vcode[DP_ENT][2];
+            uint32_t vscale[DP_ENT];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                vcode[i] = R[i].v;
-                uint32_t b2 = word(R[i].s, 2 + (qt >> 1)) >> (16 * (qt & 1)) & 0xffffu;
-                if ((b2 & 0x7fu) == 0x7fu) b2 &= 0xff00u;
-                if ((b2 & 0x7f00u) == 0x7f00u) b2 &= 0x00ffu;
-                vscale[i] = b2;
+            for (int i = 0; i < DP_ENT; ++i) {
+                vcode[i][0] = R[i].v[0];
+                vcode[i][1] = R[i].v[1];
+                vscale[i] = R[i].vs;
             }
             if (t + 1 < hi) {  // the next tile's rows, in flight while V is converted
                 if (t + 1 >= w.t1) w.next(a);
@@ -434,7 +474,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             if (n >= 2) wait(&vempty[s], ((n >> 1) - 1) & 1u);
             uint8_t* vt = smem + DP_OFF_V + (size_t)s * DP_TILE;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) store(vt, e0 + 64 * i, vcode[i], vscale[i]);
+            for (int i = 0; i < DP_ENT; ++i) store(vt + DP_STEP * 128 * i, vcode[i], vscale[i]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&vfull[s]);
@@ -495,8 +535,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                         const uint32_t b = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
                         return b & (x == 0 ? ok.x : x == 1 ? ok.y : x == 2 ? ok.z : ok.w);
                     };
-                    // ---- the row's maximum -----------------------------------------------------------
-                    float mx = -INFINITY;
+                    // ---- 32 columns at a time: maximum, P over S, the sum ---------------------------------
 #pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
                         uint32_t v[32];
@@ -508,54 +547,69 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                             for (int e = 0; e < 32; ++e)
                                 if (!((b >> e) & 1u)) v[e] = 0xff800000u;
                         }
+                        float mx[4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            mx = fmaxf(fmaxf(mx, __uint_as_float(v[e])), __uint_as_float(v[e + 1]));
-                    }
-                    mx *= c;  // log2 domain
-                    const bool rise = mx > -INFINITY && (m == -INFINITY || mx + bias > kPMax);
-                    if (__any_sync(0xffffffffu, rise)) {
-                        const float f = rise && m != -INFINITY ? ex2(m - mx) : 1.f;
-                        if (rise) {
-                            m = mx;
-                            bias = kPBias - mx;
-                            l *= f;
-                        }
-                        __syncwarp();
-                        if (t > first) {  // O is complete: S of this tile was issued after its last product
+                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 4]));
+#pragma unroll
+                        for (int e = 8; e < 32; e += 8)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                mx[y] = fmaxf(fmaxf(mx[y], __uint_as_float(v[e + y])), __uint_as_float(v[e + y + 4]));
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // log2 domain
+                        const bool rise = top > -INFINITY && (m == -INFINITY || top + bias > kPMax);
+                        if (__any_sync(0xffffffffu, rise)) {
+                            // m takes whole numbers, so O, the sum and P of the tile's earlier columns are
+                            // rescaled by a power of two, exactly
+                            const float mn = ceilf(top), f = rise && m != -INFINITY ? ex2(m - mn) : 1.f;
+                            if (rise) {
+                                m = mn;
+                                bias = kPBias - mn;
+                                l *= f;
+                            }
+                            __syncwarp();
+                            // f as two fp16 factors: it may lie below fp16's range where P times f does not
+                            const float fa = fmaxf(f, 0x1p-20f), fb = f / fa;
+                            const uint32_t ha = f2_to_h2(fa, fa), hb = f2_to_h2(fb, fb);
 #pragma unroll 1
-                            for (int x = 0; x < 4; ++x) {
-                                uint32_t v[32];
-                                tmem_ld32(tO + 32u * x, v);
+                            for (int y = 0; y < x; ++y) {
+                                uint32_t p[32];
+                                tmem_ld32(tS + 32u * y, p);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                                tmem_st32(tO + 32u * x, v);
+                                for (int e = 0; e < 32; ++e) p[e] = hmul2(hmul2(p[e], ha), hb);
+                                tmem_st32(tS + 32u * y, p);
                             }
-                        }
-                    }
-                    // ---- P over S, the sum -------------------------------------------------------------
+                            if (t > first) {  // O is complete: S of this tile was issued after its last product
 #pragma unroll 1
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t v[32], p[16], q[16];
-                        tmem_ld32(tS + 32u * x, v);
-                        tmem_wait_ld();
-                        const uint32_t b = all ? ~0u : cols(x);
-                        float s0 = 0.f, s1 = 0.f;
+                                for (int y = 0; y < 4; ++y) {
+                                    uint32_t o[32];
+                                    tmem_ld32(tO + 32u * y, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st32(tO + 32u * y, o);
+                                }
+                            }
+                            tmem_wait_st();
+                        }
+                        uint32_t p[16], q[16];
+                        // two columns per packed operation
+                        const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(bias, bias);
+                        uint64_t s0 = 0, s1 = 0;
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            float p0 = ex2(fmaf(__uint_as_float(v[e]), c, bias));
-                            float p1 = ex2(fmaf(__uint_as_float(v[e + 1]), c, bias));
-                            if (!all) {
-                                if (!((b >> e) & 1u)) p0 = 0.f;
-                                if (!((b >> e) & 2u)) p1 = 0.f;
-                            }
-                            s0 += p0;
-                            s1 += p1;
+                            float p0, p1;
+                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, bb), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            if (e & 2) s1 = add_f32x2(s1, pack_f32x2(p0, p1));
+                            else s0 = add_f32x2(s0, pack_f32x2(p0, p1));
                             p[e >> 1] = f2_to_h2(p0, p1);
                             if (SPLIT) q[e >> 1] = rest_h2(p0, p1, p[e >> 1]);
                         }
-                        l += s0 + s1;
+                        float l0, l1;
+                        unpack_f32x2(add_f32x2(s0, s1), l0, l1);
+                        l += l0 + l1;
                         tmem_st16(tS + 32u * x, p);
                         if (SPLIT) tmem_st16(tS + 32u * x + 16u, q);
                     }
