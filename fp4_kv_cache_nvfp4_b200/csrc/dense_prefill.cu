@@ -148,21 +148,32 @@ struct Walk {
 };
 
 // ---- tensor-core helpers --------------------------------------------------------------
+// Descriptors as two words, so that a step along K is one addition to the low
+// one (see umma_desc_sw128, umma_desc_sw128_mn): the thread that issues the
+// products has little time for address arithmetic.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (uint32_t)umma_desc_sw128(saddr); }
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr) { return (uint32_t)umma_desc_sw128_mn(saddr, DP_HALF); }
 // D[128 x 128] (+)= A . B with fp16 operands, A in shared memory
-__device__ __forceinline__ void dp_mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t acc) {
+__device__ __forceinline__ void dp_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
-        "l"(da), "l"(db), "r"(kIdescS), "r"(acc), "r"(0u)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kIdescS), "r"(kDescHi), "r"(acc)
         : "memory");
 }
 // the same with A in TMEM (rows = lanes, two fp16 per column) and B transposed
-__device__ __forceinline__ void dp_mma_ts(uint32_t d, uint32_t ta, uint64_t db, uint32_t acc) {
+__device__ __forceinline__ void dp_mma_ts(uint32_t d, uint32_t ta, uint32_t b, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(d),
-        "r"(ta), "l"(db), "r"(kIdescPV), "r"(acc), "r"(0u)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(ta), "r"(b), "r"(kIdescPV), "r"(kDescHi), "r"(acc)
         : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 // 32 consecutive columns of this thread's lane
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
@@ -290,79 +301,103 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         }
     }
     __syncthreads();
-    auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; after one timeout every wait returns at once
-        if (*s_timeout) return;
-        if (!mbar_wait(bar, parity, kDenseWaitLimit)) *s_timeout = 1;
+    // bounded; a thread that gave up once does not wait any more
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity, kDenseWaitLimit)) {
+            dead = true;
+            *s_timeout = 1;
+        }
     };
 
     if (lo < hi && wid == DP_W_MMA) {
-        // ================= the products =================
-        if (lane == 0) {
-            Walk w;
-            w.start(a, misc + 2);
-            uint32_t kn = 0, vn = 0, seg = 0, seg1 = 0, pn[2] = {0, 0};  // tiles, units (with a second row tile), P tiles so far
-            const uint32_t qaddr = smem_u32(smem + DP_OFF_Q), kaddr = smem_u32(smem + DP_OFF_K), vaddr = smem_u32(smem + DP_OFF_V);
-            auto mma_s = [&](int i) {  // S of row tile i over K tile kn
-                const uint32_t q = qaddr + (uint32_t)i * DP_TILE, k = kaddr + (kn & 1u) * DP_TILE;
+        // ================= the products: every lane keeps the books, one issues =================
+        const bool leader = elect_one();
+        Walk w;
+        w.start(a, misc + 2);
+        uint32_t ks = 0, kph = 0, vs = 0, vph = 0, qph = 0, qph1 = 0, pph0 = 0, pph1 = 0;  // slots and phases
+        const uint32_t qlo = desc_lo(smem_u32(smem + DP_OFF_Q)), klo = desc_lo(smem_u32(smem + DP_OFF_K)),
+                       vlo = desc_lo_mn(smem_u32(smem + DP_OFF_V));
+        auto mma_s = [&](int i) {  // S of row tile i over the K tile in slot ks
+            if (leader) {
+                const uint32_t q = qlo + (uint32_t)i * (DP_TILE >> 4), k = klo + ks * (DP_TILE >> 4);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    dp_mma_ss(tmem + 128u * i, umma_desc_sw128(q + (ks >> 2) * DP_HALF) + 2u * (ks & 3),
-                              umma_desc_sw128(k + (ks >> 2) * DP_HALF) + 2u * (ks & 3), ks > 0);
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t o = (uint32_t)(x >> 2) * (DP_HALF >> 4) + 2u * (x & 3);
+                    dp_mma_ss(tmem + 128u * i, q + o, k + o, x > 0);
+                }
                 umma_commit(&sfull[i]);
-            };
-            auto mma_pv = [&](int i, bool first) {  // O of row tile i += P . V tile vn
-                wait(&pfull[i], pn[i] & 1u);
-                ++pn[i];
-                tc_fence_after();
-                const uint32_t v = vaddr + (vn & 1u) * DP_TILE, p = tmem + 128u * i, o = tmem + 256u + 128u * i;
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {  // P of 16 entries: 8 columns
-                    const uint64_t db = umma_desc_sw128_mn(v + ks * 2048u, DP_HALF);
-                    dp_mma_ts(o, p + 32u * (ks >> 1) + 8u * (ks & 1), db, !(first && ks == 0));
-                    if (SPLIT) dp_mma_ts(o, p + 32u * (ks >> 1) + 16u + 8u * (ks & 1), db, 1);
-                }
-            };
-            for (uint32_t t = lo; t < hi;) {
-                const uint32_t end = min(hi, w.t1);
-                const bool two = w.tokens() > DP_TOK / 2;
-                wait(&qfull[0], seg & 1u);
-                if (two) wait(&qfull[1], seg1 & 1u);
-                wait(&kfull[kn & 1u], (kn >> 1) & 1u);
-                tc_fence_after();
-                mma_s(0);
-                if (two) mma_s(1);
-                umma_commit(&kempty[kn & 1u]);
-                ++kn;
-                for (const uint32_t first = t; t < end; ++t) {
-                    const bool more = t + 1 < end;
-                    wait(&vfull[vn & 1u], (vn >> 1) & 1u);
-                    mma_pv(0, t == first);
-                    if (more) {
-                        wait(&kfull[kn & 1u], (kn >> 1) & 1u);
-                        tc_fence_after();
-                        mma_s(0);
-                    } else {
-                        umma_commit(&ofull[0]);
-                    }
-                    if (two) mma_pv(1, t == first);
-                    umma_commit(&vempty[vn & 1u]);
-                    ++vn;
-                    if (more) {
-                        if (two) mma_s(1);
-                        umma_commit(&kempty[kn & 1u]);
-                        ++kn;
-                    } else if (two) {
-                        umma_commit(&ofull[1]);
-                    }
-                }
-                ++seg;
-                seg1 += two;
-                if (t < hi) w.next(a);
             }
-            umma_commit(mma_done);
-            if (!mbar_wait(mma_done, 0u, kDenseWaitLimit)) *s_timeout = 1;
+            __syncwarp();
+        };
+        auto mma_pv = [&](int i, bool first) {  // O of row tile i += P . V tile in slot vs
+            if (leader) {
+                const uint32_t v = vlo + vs * (DP_TILE >> 4), p = tmem + 128u * i, o = tmem + 256u + 128u * i;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {  // P of 16 entries: 8 columns
+                    dp_mma_ts(o, p + 32u * (x >> 1) + 8u * (x & 1), v + 128u * x, x > 0 || !first);
+                    if (SPLIT) dp_mma_ts(o, p + 32u * (x >> 1) + 16u + 8u * (x & 1), v + 128u * x, 1);
+                }
+            }
+            __syncwarp();
+        };
+        auto commit = [&](uint64_t* bar) {
+            if (leader) umma_commit(bar);
+            __syncwarp();
+        };
+        auto next_k = [&]() {
+            commit(&kempty[ks]);
+            ks ^= 1u;
+            kph ^= ks == 0;
+        };
+        for (uint32_t t = lo; t < hi;) {
+            const uint32_t end = min(hi, w.t1);
+            const bool two = w.tokens() > DP_TOK / 2;
+            wait(&qfull[0], qph);
+            qph ^= 1u;
+            if (two) {
+                wait(&qfull[1], qph1);
+                qph1 ^= 1u;
+            }
+            wait(&kfull[ks], kph);
+            tc_fence_after();
+            mma_s(0);
+            if (two) mma_s(1);
+            next_k();
+            for (const uint32_t first = t; t < end; ++t) {
+                const bool more = t + 1 < end;
+                wait(&vfull[vs], vph);
+                wait(&pfull[0], pph0);
+                pph0 ^= 1u;
+                tc_fence_after();
+                mma_pv(0, t == first);
+                if (more) {
+                    wait(&kfull[ks], kph);
+                    tc_fence_after();
+                    mma_s(0);
+                } else {
+                    commit(&ofull[0]);
+                }
+                if (two) {
+                    wait(&pfull[1], pph1);
+                    pph1 ^= 1u;
+                    tc_fence_after();
+                    mma_pv(1, t == first);
+                }
+                commit(&vempty[vs]);
+                vs ^= 1u;
+                vph ^= vs == 0;
+                if (more) {
+                    if (two) mma_s(1);
+                    next_k();
+                } else if (two) {
+                    commit(&ofull[1]);
+                }
+            }
+            if (t < hi) w.next(a);
         }
-        __syncwarp();
+        commit(mma_done);
+        if (!mbar_wait(mma_done, 0u, kDenseWaitLimit)) *s_timeout = 1;
     } else if (lo < hi && wid >= DP_W_CONV) {
         // ================= converters: FP4 rows -> fp16 operand tiles =================
         // Thread ct owns quarter qt (32 channels of K and of V) of entries e0 + DP_STEP i.
