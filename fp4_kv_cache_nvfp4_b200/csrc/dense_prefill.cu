@@ -47,13 +47,13 @@ constexpr size_t DP_OFF_K = DP_OFF_Q + 2 * DP_TILE;       // [2 slots]
 constexpr size_t DP_OFF_V = DP_OFF_K + 2 * DP_TILE;       // [2 slots]
 constexpr size_t DP_OFF_OK = DP_OFF_V + 2 * DP_TILE;      // [4][16 B]: one bit per entry of a K tile, 0: missing page
 constexpr size_t DP_OFF_BAR = DP_OFF_OK + 64;
-constexpr int DP_NBAR = 4 * 2 + 4 * 2 + 1;
+constexpr int DP_NBAR = 4 * 2 + 2 + 4 + 4 + 2 + 2 + 1;
 constexpr size_t DP_OFF_SCAN = DP_OFF_BAR + DP_NBAR * 8;  // [64] words
 constexpr size_t DP_OFF_MISC = DP_OFF_SCAN + 256;         // tmem base, timeout flag, start sequence, unit, its first tile
 constexpr size_t DP_SMEM = DP_OFF_MISC + 32 + 1024;       // + slack for the 1 KiB alignment
 static_assert(DP_OFF_BAR % 8 == 0 && DP_SMEM <= 227 * 1024, "dense prefill layout");
-constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-constexpr uint32_t kIdescPV = kIdescS | (1u << 16);  // B (V) has its dims contiguous
+constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(64 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);  // V: its dims contiguous
 
 struct PrefillDenseArgs {
     DenseArgs a;
@@ -154,7 +154,7 @@ struct Walk {
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (uint32_t)umma_desc_sw128(saddr); }
 __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr) { return (uint32_t)umma_desc_sw128_mn(saddr, DP_HALF); }
-// D[128 x 128] (+)= A . B with fp16 operands, A in shared memory
+// D[128 x 64] (+)= A . B with fp16 operands, A in shared memory
 __device__ __forceinline__ void dp_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
@@ -162,7 +162,7 @@ __device__ __forceinline__ void dp_mma_ss(uint32_t d, uint32_t a, uint32_t b, ui
         "r"(a), "r"(b), "r"(kIdescS), "r"(kDescHi), "r"(acc)
         : "memory");
 }
-// the same with A in TMEM (rows = lanes, two fp16 per column) and B transposed
+// D[128 x 128] (+)= A . B, A in TMEM (rows = lanes, two fp16 per column), B transposed
 __device__ __forceinline__ void dp_mma_ts(uint32_t d, uint32_t ta, uint32_t b, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %4};\n\t"
@@ -234,9 +234,10 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
     uint64_t* vfull = kempty + 2;
     uint64_t* vempty = vfull + 2;
     uint64_t* qfull = vempty + 2;   // [2] a row tile's Q written (4 softmax warps)
-    uint64_t* sfull = qfull + 2;    // [2] S complete (commit)
-    uint64_t* pfull = sfull + 2;    // [2] P written, O rescaled (4 softmax warps)
-    uint64_t* ofull = pfull + 2;    // [2] O of a unit complete (commit)
+    uint64_t* sfull = qfull + 2;    // [2][2 halves] S complete (commit)
+    uint64_t* pfull = sfull + 4;    // [2][2] P written, O rescaled (4 softmax warps)
+    uint64_t* pvdone = pfull + 4;   // [2] a half's products with V complete (commit)
+    uint64_t* ofull = pvdone + 2;   // [2] O of a unit complete (commit)
     uint64_t* mma_done = ofull + 2;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + DP_OFF_MISC);
     volatile uint32_t* s_timeout = misc + 1;
@@ -248,8 +249,11 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             mbar_init(&vfull[i], DP_NCONV);
             mbar_init(&vempty[i], 1);
             mbar_init(&qfull[i], 4);
-            mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sfull[2 * i + h], 1);
+                mbar_init(&pfull[2 * i + h], 4);
+            }
+            mbar_init(&pvdone[i], 1);
             mbar_init(&ofull[i], 1);
         }
         mbar_init(mma_done, 1);
@@ -318,26 +322,28 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         uint32_t ks = 0, kph = 0, vs = 0, vph = 0, qph = 0, qph1 = 0, pph0 = 0, pph1 = 0;  // slots and phases
         const uint32_t qlo = desc_lo(smem_u32(smem + DP_OFF_Q)), klo = desc_lo(smem_u32(smem + DP_OFF_K)),
                        vlo = desc_lo_mn(smem_u32(smem + DP_OFF_V));
-        auto mma_s = [&](int i) {  // S of row tile i over the K tile in slot ks
+        auto mma_s = [&](int i, int h) {  // S of row tile i over half h of the K tile in slot ks
             if (leader) {
-                const uint32_t q = qlo + (uint32_t)i * (DP_TILE >> 4), k = klo + ks * (DP_TILE >> 4);
+                const uint32_t q = qlo + (uint32_t)i * (DP_TILE >> 4), k = klo + ks * (DP_TILE >> 4) + (uint32_t)h * (64u * 128u >> 4);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const uint32_t o = (uint32_t)(x >> 2) * (DP_HALF >> 4) + 2u * (x & 3);
-                    dp_mma_ss(tmem + 128u * i, q + o, k + o, x > 0);
+                    dp_mma_ss(tmem + 128u * i + 64u * h, q + o, k + o, x > 0);
                 }
-                umma_commit(&sfull[i]);
+                umma_commit(&sfull[2 * i + h]);
             }
             __syncwarp();
         };
-        auto mma_pv = [&](int i, bool first) {  // O of row tile i += P . V tile in slot vs
+        auto mma_pv = [&](int i, int h, bool first) {  // O of row tile i += P . V over half h of the tile in slot vs
             if (leader) {
                 const uint32_t v = vlo + vs * (DP_TILE >> 4), p = tmem + 128u * i, o = tmem + 256u + 128u * i;
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {  // P of 16 entries: 8 columns
+                for (int y = 0; y < 4; ++y) {  // P of 16 entries: 8 columns
+                    const int x = 4 * h + y;
                     dp_mma_ts(o, p + 32u * (x >> 1) + 8u * (x & 1), v + 128u * x, x > 0 || !first);
                     if (SPLIT) dp_mma_ts(o, p + 32u * (x >> 1) + 16u + 8u * (x & 1), v + 128u * x, 1);
                 }
+                umma_commit(&pvdone[i]);
             }
             __syncwarp();
         };
@@ -361,37 +367,46 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             }
             wait(&kfull[ks], kph);
             tc_fence_after();
-            mma_s(0);
-            if (two) mma_s(1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mma_s(0, h);
+                if (two) mma_s(1, h);
+            }
             next_k();
+            // A half's P gives way to the same half of the next tile's S, while the softmax
+            // works on the other half: it waits for no product unless the tensor core is behind.
             for (const uint32_t first = t; t < end; ++t) {
                 const bool more = t + 1 < end;
                 wait(&vfull[vs], vph);
-                wait(&pfull[0], pph0);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    wait(&pfull[h], pph0);
+                    tc_fence_after();
+                    mma_pv(0, h, t == first);
+                    if (more) {
+                        if (h == 0) {
+                            wait(&kfull[ks], kph);
+                            tc_fence_after();
+                        }
+                        mma_s(0, h);
+                    }
+                    if (two) {
+                        wait(&pfull[2 + h], pph1);
+                        tc_fence_after();
+                        mma_pv(1, h, t == first);
+                        if (more) mma_s(1, h);
+                    }
+                }
                 pph0 ^= 1u;
-                tc_fence_after();
-                mma_pv(0, t == first);
-                if (more) {
-                    wait(&kfull[ks], kph);
-                    tc_fence_after();
-                    mma_s(0);
-                } else {
-                    commit(&ofull[0]);
-                }
-                if (two) {
-                    wait(&pfull[1], pph1);
-                    pph1 ^= 1u;
-                    tc_fence_after();
-                    mma_pv(1, t == first);
-                }
+                if (two) pph1 ^= 1u;
                 commit(&vempty[vs]);
                 vs ^= 1u;
                 vph ^= vs == 0;
                 if (more) {
-                    if (two) mma_s(1);
                     next_k();
-                } else if (two) {
-                    commit(&ofull[1]);
+                } else {
+                    commit(&ofull[0]);
+                    if (two) commit(&ofull[1]);
                 }
             }
             if (t < hi) w.next(a);
@@ -559,7 +574,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 }
                 float m = -INFINITY, bias = kPBias, l = 0.f;
                 for (; t < end; ++t, ++n, ++sn) {
-                    wait(&sfull[i], sn & 1u);
+                    wait(&sfull[2 * i], sn & 1u);
                     tc_fence_after();
                     const int nv = seen - (int)(t - w.t0) * DP_KEYS;  // entries of the tile this row sees
                     const uint4 ok = *reinterpret_cast<const uint4*>(smem + DP_OFF_OK + (n & 3u) * 16);
@@ -573,6 +588,14 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     // ---- 32 columns at a time: maximum, P over S, the sum ---------------------------------
 #pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
+                        if (x == 2) {  // the first half's P is out
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&pfull[2 * i]);
+                            wait(&sfull[2 * i + 1], sn & 1u);
+                            tc_fence_after();
+                        }
                         uint32_t v[32];
                         tmem_ld32(tS + 32u * x, v);
                         tmem_wait_ld();
@@ -606,7 +629,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                             const float fa = fmaxf(f, 0x1p-20f), fb = f / fa;
                             const uint32_t ha = f2_to_h2(fa, fa), hb = f2_to_h2(fb, fb);
 #pragma unroll 1
-                            for (int y = 0; y < x; ++y) {
+                            for (int y = x & 2; y < x; ++y) {  // (the other half's is with the products)
                                 uint32_t p[32];
                                 tmem_ld32(tS + 32u * y, p);
                                 tmem_wait_ld();
@@ -614,7 +637,9 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                                 for (int e = 0; e < 32; ++e) p[e] = hmul2(hmul2(p[e], ha), hb);
                                 tmem_st32(tS + 32u * y, p);
                             }
-                            if (t > first) {  // O is complete: S of this tile was issued after its last product
+                            if (t > first || x >= 2) {  // O holds something: once its last products are done
+                                wait(&pvdone[i], (2u * sn + (uint32_t)(x >> 1) + 1u) & 1u);
+                                tc_fence_after();
 #pragma unroll 1
                                 for (int y = 0; y < 4; ++y) {
                                     uint32_t o[32];
@@ -651,7 +676,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[i]);
+                    if (lane == 0) mbar_arrive(&pfull[2 * i + 1]);
                 }
                 // ---- the unit's rows ---------------------------------------------------------------
                 wait(&ofull[i], units & 1u);
