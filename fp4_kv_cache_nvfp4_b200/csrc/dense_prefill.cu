@@ -47,13 +47,13 @@ constexpr size_t DP_OFF_K = DP_OFF_Q + 2 * DP_TILE;       // [2 slots]
 constexpr size_t DP_OFF_V = DP_OFF_K + 2 * DP_TILE;       // [2 slots]
 constexpr size_t DP_OFF_OK = DP_OFF_V + 2 * DP_TILE;      // [4][16 B]: one bit per entry of a K tile, 0: missing page
 constexpr size_t DP_OFF_BAR = DP_OFF_OK + 64;
-constexpr int DP_NBAR = 4 * 2 + 2 + 4 + 4 + 2 + 2 + 1;
+constexpr int DP_NBAR = 4 * 2 + 4 * 2 + 1;
 constexpr size_t DP_OFF_SCAN = DP_OFF_BAR + DP_NBAR * 8;  // [64] words
 constexpr size_t DP_OFF_MISC = DP_OFF_SCAN + 256;         // tmem base, timeout flag, start sequence, unit, its first tile
 constexpr size_t DP_SMEM = DP_OFF_MISC + 32 + 1024;       // + slack for the 1 KiB alignment
 static_assert(DP_OFF_BAR % 8 == 0 && DP_SMEM <= 227 * 1024, "dense prefill layout");
-constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(64 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);  // V: its dims contiguous
+constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdescS | (1u << 16);  // B (V) has its dims contiguous
 
 struct PrefillDenseArgs {
     DenseArgs a;
@@ -154,7 +154,7 @@ struct Walk {
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (uint32_t)umma_desc_sw128(saddr); }
 __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr) { return (uint32_t)umma_desc_sw128_mn(saddr, DP_HALF); }
-// D[128 x 64] (+)= A . B with fp16 operands, A in shared memory
+// D[128 x 128] (+)= A . B with fp16 operands, A in shared memory
 __device__ __forceinline__ void dp_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
@@ -162,7 +162,7 @@ __device__ __forceinline__ void dp_mma_ss(uint32_t d, uint32_t a, uint32_t b, ui
         "r"(a), "r"(b), "r"(kIdescS), "r"(kDescHi), "r"(acc)
         : "memory");
 }
-// D[128 x 128] (+)= A . B, A in TMEM (rows = lanes, two fp16 per column), B transposed
+// the same with A in TMEM (rows = lanes, two fp16 per column) and B transposed
 __device__ __forceinline__ void dp_mma_ts(uint32_t d, uint32_t ta, uint32_t b, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %4};\n\t"
@@ -186,21 +186,28 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&v)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
+          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+          "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+        : "r"(addr));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
         "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
         "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(v[0]),
-        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr)
         : "memory");
 }
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
@@ -234,10 +241,9 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
     uint64_t* vfull = kempty + 2;
     uint64_t* vempty = vfull + 2;
     uint64_t* qfull = vempty + 2;   // [2] a row tile's Q written (4 softmax warps)
-    uint64_t* sfull = qfull + 2;    // [2][2 halves] S complete (commit)
-    uint64_t* pfull = sfull + 4;    // [2][2] P written, O rescaled (4 softmax warps)
-    uint64_t* pvdone = pfull + 4;   // [2] a half's products with V complete (commit)
-    uint64_t* ofull = pvdone + 2;   // [2] O of a unit complete (commit)
+    uint64_t* sfull = qfull + 2;    // [2] S complete (commit)
+    uint64_t* pfull = sfull + 2;    // [2] P written, O rescaled (4 softmax warps)
+    uint64_t* ofull = pfull + 2;    // [2] O of a unit complete (commit)
     uint64_t* mma_done = ofull + 2;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + DP_OFF_MISC);
     volatile uint32_t* s_timeout = misc + 1;
@@ -249,11 +255,8 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             mbar_init(&vfull[i], DP_NCONV);
             mbar_init(&vempty[i], 1);
             mbar_init(&qfull[i], 4);
-            for (int h = 0; h < 2; ++h) {
-                mbar_init(&sfull[2 * i + h], 1);
-                mbar_init(&pfull[2 * i + h], 4);
-            }
-            mbar_init(&pvdone[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
             mbar_init(&ofull[i], 1);
         }
         mbar_init(mma_done, 1);
@@ -322,28 +325,26 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         uint32_t ks = 0, kph = 0, vs = 0, vph = 0, qph = 0, qph1 = 0, pph0 = 0, pph1 = 0;  // slots and phases
         const uint32_t qlo = desc_lo(smem_u32(smem + DP_OFF_Q)), klo = desc_lo(smem_u32(smem + DP_OFF_K)),
                        vlo = desc_lo_mn(smem_u32(smem + DP_OFF_V));
-        auto mma_s = [&](int i, int h) {  // S of row tile i over half h of the K tile in slot ks
+        auto mma_s = [&](int i) {  // S of row tile i over the K tile in slot ks
             if (leader) {
-                const uint32_t q = qlo + (uint32_t)i * (DP_TILE >> 4), k = klo + ks * (DP_TILE >> 4) + (uint32_t)h * (64u * 128u >> 4);
+                const uint32_t q = qlo + (uint32_t)i * (DP_TILE >> 4), k = klo + ks * (DP_TILE >> 4);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const uint32_t o = (uint32_t)(x >> 2) * (DP_HALF >> 4) + 2u * (x & 3);
-                    dp_mma_ss(tmem + 128u * i + 64u * h, q + o, k + o, x > 0);
+                    dp_mma_ss(tmem + 128u * i, q + o, k + o, x > 0);
                 }
-                umma_commit(&sfull[2 * i + h]);
+                umma_commit(&sfull[i]);
             }
             __syncwarp();
         };
-        auto mma_pv = [&](int i, int h, bool first) {  // O of row tile i += P . V over half h of the tile in slot vs
+        auto mma_pv = [&](int i, bool first) {  // O of row tile i += P . V tile in slot vs
             if (leader) {
                 const uint32_t v = vlo + vs * (DP_TILE >> 4), p = tmem + 128u * i, o = tmem + 256u + 128u * i;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {  // P of 16 entries: 8 columns
-                    const int x = 4 * h + y;
+                for (int x = 0; x < 8; ++x) {  // P of 16 entries: 8 columns
                     dp_mma_ts(o, p + 32u * (x >> 1) + 8u * (x & 1), v + 128u * x, x > 0 || !first);
                     if (SPLIT) dp_mma_ts(o, p + 32u * (x >> 1) + 16u + 8u * (x & 1), v + 128u * x, 1);
                 }
-                umma_commit(&pvdone[i]);
             }
             __syncwarp();
         };
@@ -367,46 +368,37 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             }
             wait(&kfull[ks], kph);
             tc_fence_after();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mma_s(0, h);
-                if (two) mma_s(1, h);
-            }
+            mma_s(0);
+            if (two) mma_s(1);
             next_k();
-            // A half's P gives way to the same half of the next tile's S, while the softmax
-            // works on the other half: it waits for no product unless the tensor core is behind.
             for (const uint32_t first = t; t < end; ++t) {
                 const bool more = t + 1 < end;
                 wait(&vfull[vs], vph);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    wait(&pfull[h], pph0);
-                    tc_fence_after();
-                    mma_pv(0, h, t == first);
-                    if (more) {
-                        if (h == 0) {
-                            wait(&kfull[ks], kph);
-                            tc_fence_after();
-                        }
-                        mma_s(0, h);
-                    }
-                    if (two) {
-                        wait(&pfull[2 + h], pph1);
-                        tc_fence_after();
-                        mma_pv(1, h, t == first);
-                        if (more) mma_s(1, h);
-                    }
-                }
+                wait(&pfull[0], pph0);
                 pph0 ^= 1u;
-                if (two) pph1 ^= 1u;
+                tc_fence_after();
+                mma_pv(0, t == first);
+                if (more) {
+                    wait(&kfull[ks], kph);
+                    tc_fence_after();
+                    mma_s(0);
+                } else {
+                    commit(&ofull[0]);
+                }
+                if (two) {
+                    wait(&pfull[1], pph1);
+                    pph1 ^= 1u;
+                    tc_fence_after();
+                    mma_pv(1, t == first);
+                }
                 commit(&vempty[vs]);
                 vs ^= 1u;
                 vph ^= vs == 0;
                 if (more) {
+                    if (two) mma_s(1);
                     next_k();
-                } else {
-                    commit(&ofull[0]);
-                    if (two) commit(&ofull[1]);
+                } else if (two) {
+                    commit(&ofull[1]);
                 }
             }
             if (t < hi) w.next(a);
@@ -574,42 +566,30 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 }
                 float m = -INFINITY, bias = kPBias, l = 0.f;
                 for (; t < end; ++t, ++n, ++sn) {
-                    wait(&sfull[2 * i], sn & 1u);
+                    wait(&sfull[i], sn & 1u);
                     tc_fence_after();
                     const int nv = seen - (int)(t - w.t0) * DP_KEYS;  // entries of the tile this row sees
                     const uint4 ok = *reinterpret_cast<const uint4*>(smem + DP_OFF_OK + (n & 3u) * 16);
                     const bool all = __all_sync(0xffffffffu, nv >= DP_KEYS && (ok.x & ok.y & ok.z & ok.w) == ~0u);
-                    // the columns of chunk x that this row sees, one bit each
-                    auto cols = [&](int x) -> uint32_t {
-                        const int k = nv - 32 * x;
-                        const uint32_t b = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
-                        return b & (x == 0 ? ok.x : x == 1 ? ok.y : x == 2 ? ok.z : ok.w);
-                    };
-                    // ---- 32 columns at a time: maximum, P over S, the sum ---------------------------------
+                    // ---- 64 columns at a time: maximum, P over S, the sum ---------------------------------
 #pragma unroll 1
-                    for (int x = 0; x < 4; ++x) {
-                        if (x == 2) {  // the first half's P is out
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&pfull[2 * i]);
-                            wait(&sfull[2 * i + 1], sn & 1u);
-                            tc_fence_after();
-                        }
-                        uint32_t v[32];
-                        tmem_ld32(tS + 32u * x, v);
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t v[64];
+                        tmem_ld64(tS + 64u * x, v);
                         tmem_wait_ld();
-                        if (!all) {
-                            const uint32_t b = cols(x);
+                        if (!all) {  // the columns that this row sees, one bit each
+                            const int k = nv - 64 * x;
+                            uint64_t b = k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1ull;
+                            b &= x == 0 ? (uint64_t)ok.x | (uint64_t)ok.y << 32 : (uint64_t)ok.z | (uint64_t)ok.w << 32;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                            for (int e = 0; e < 64; ++e)
                                 if (!((b >> e) & 1u)) v[e] = 0xff800000u;
                         }
                         float mx[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 4]));
 #pragma unroll
-                        for (int e = 8; e < 32; e += 8)
+                        for (int e = 8; e < 64; e += 8)
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
                                 mx[y] = fmaxf(fmaxf(mx[y], __uint_as_float(v[e + y])), __uint_as_float(v[e + y + 4]));
@@ -628,55 +608,59 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                             // f as two fp16 factors: it may lie below fp16's range where P times f does not
                             const float fa = fmaxf(f, 0x1p-20f), fb = f / fa;
                             const uint32_t ha = f2_to_h2(fa, fa), hb = f2_to_h2(fb, fb);
+                            if (x == 1) {
 #pragma unroll 1
-                            for (int y = x & 2; y < x; ++y) {  // (the other half's is with the products)
-                                uint32_t p[32];
-                                tmem_ld32(tS + 32u * y, p);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) p[e] = hmul2(hmul2(p[e], ha), hb);
-                                tmem_st32(tS + 32u * y, p);
-                            }
-                            if (t > first || x >= 2) {  // O holds something: once its last products are done
-                                wait(&pvdone[i], (2u * sn + (uint32_t)(x >> 1) + 1u) & 1u);
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int y = 0; y < 4; ++y) {
-                                    uint32_t o[32];
-                                    tmem_ld32(tO + 32u * y, o);
+                                for (int y = 0; y < 64; y += 16) {
+                                    uint32_t p[16];
+                                    tmem_ld16(tS + y, p);
                                     tmem_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st32(tO + 32u * y, o);
+                                    for (int e = 0; e < 16; ++e) p[e] = hmul2(hmul2(p[e], ha), hb);
+                                    tmem_st16(tS + y, p);
+                                }
+                            }
+                            if (t > first) {  // O is complete: S of this tile was issued after its last product
+#pragma unroll 1
+                                for (int y = 0; y < 128; y += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tO + y, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st16(tO + y, o);
                                 }
                             }
                             tmem_wait_st();
                         }
-                        uint32_t p[16], q[16];
                         // two columns per packed operation
                         const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(bias, bias);
                         uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float p0, p1;
-                            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, bb), p0, p1);
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            if (e & 2) s1 = add_f32x2(s1, pack_f32x2(p0, p1));
-                            else s0 = add_f32x2(s0, pack_f32x2(p0, p1));
-                            p[e >> 1] = f2_to_h2(p0, p1);
-                            if (SPLIT) q[e >> 1] = rest_h2(p0, p1, p[e >> 1]);
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t p[16], q[16];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float p0, p1;
+                                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[32 * g + e]), __uint_as_float(v[32 * g + e + 1])), cc, bb),
+                                             p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                if (e & 2) s1 = add_f32x2(s1, pack_f32x2(p0, p1));
+                                else s0 = add_f32x2(s0, pack_f32x2(p0, p1));
+                                p[e >> 1] = f2_to_h2(p0, p1);
+                                if (SPLIT) q[e >> 1] = rest_h2(p0, p1, p[e >> 1]);
+                            }
+                            tmem_st16(tS + 64u * x + 32u * g, p);
+                            if (SPLIT) tmem_st16(tS + 64u * x + 32u * g + 16u, q);
                         }
                         float l0, l1;
                         unpack_f32x2(add_f32x2(s0, s1), l0, l1);
                         l += l0 + l1;
-                        tmem_st16(tS + 32u * x, p);
-                        if (SPLIT) tmem_st16(tS + 32u * x + 16u, q);
                     }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[2 * i + 1]);
+                    if (lane == 0) mbar_arrive(&pfull[i]);
                 }
                 // ---- the unit's rows ---------------------------------------------------------------
                 wait(&ofull[i], units & 1u);
