@@ -83,7 +83,7 @@ csa2_status csa2_dense_attn_prefill(const csa2_layer_desc* desc, const csa2_kv_c
     if (s != CSA2_OK || B == 0 || T == 0) return s;
     a.cu_q = cu_q;
     a.q_start = q_start;
-    if (((int64_t)T / 16 + B) * ((max_len + 127) / 128) > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    if (((int64_t)T / 16 + B) * ((max_len + 127) / 128 + 1) > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     return from_cuda(launch_dense_prefill(a, static_cast<char*>(workspace), (cudaStream_t)stream));
 }
 

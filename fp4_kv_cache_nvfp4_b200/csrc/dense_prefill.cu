@@ -24,6 +24,8 @@
 // tensor core, the 16,384 exponentials 1024 cycles of the special-function
 // units, and the products' operands with the dequantised tiles' writes about 1000
 // cycles of shared memory, so three units are near their limits at once.
+#include <string.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -60,7 +62,7 @@ struct PrefillDenseArgs {
     float* part_o;  // [2 * ctas][256 rows][128], times 2^(kPBias - m)
     float* part_m;  // [2 * ctas][256]
     float* part_l;  // [2 * ctas][256]
-    int4* cut;      // [2 * ctas]: (first row token, tokens, first tile, end), (first tile of this CTA) of the unit it begins inside
+    int4* cut;      // [2 * ctas]: (first row token, tokens, first place, end of the tiles), (first place of this CTA) of the unit it begins inside
 };
 
 // ---- which units and tiles ----------------------------------------------------------
@@ -96,10 +98,12 @@ __device__ __forceinline__ int seen_by(const DenseArgs& a, const SeqQ& s, int i)
 __device__ __forceinline__ uint32_t unit_tiles(const DenseArgs& a, const SeqQ& s, int k) {
     return max(1u, (uint32_t)(seen_by(a, s, min((k + 1) * DP_TOK, s.nq) - 1) + DP_KEYS - 1) / DP_KEYS);
 }
-// Tiles of the units before k.  With A = p0 + 16 + 127 r and D = 128 r, a full
-// unit i has min(C, floor((A + 16 i) / D)) tiles, C = ceil(len / 128): a staircase,
-// whose sum is a difference of G(x) = sum_{j < x} floor(j / (8 r)).
-__device__ __forceinline__ uint64_t tiles_before(const DenseArgs& a, const SeqQ& s, int k) {
+// Places in the list of the units before k: a unit takes one for each tile and
+// one for what it costs besides (its Q, its rows: as long as a tile or two, which
+// counts where the units are short).  With A = p0 + 16 + 127 r and D = 128 r, a
+// full unit i has min(C, floor((A + 16 i) / D)) tiles, C = ceil(len / 128): a
+// staircase, whose sum is a difference of G(x) = sum_{j < x} floor(j / (8 r)).
+__device__ __forceinline__ uint64_t places_before(const DenseArgs& a, const SeqQ& s, int k) {
     if (k <= 0) return 0;
     const int last = s.units() - 1;
     const uint64_t C = max(1u, (uint32_t)(s.len + DP_KEYS - 1) / DP_KEYS);
@@ -108,33 +112,34 @@ __device__ __forceinline__ uint64_t tiles_before(const DenseArgs& a, const SeqQ&
     if (!a.q_start) {
         n = (uint64_t)m * C;
     } else {
-        const int64_t r = a.ratio, A = s.p0 + DP_TOK + 127 * r, D = 128 * r, M = D / DP_TOK, x = A / DP_TOK;
-        int64_t ic = ((int64_t)C * D - A + DP_TOK - 1) / DP_TOK;  // the first unit with C
+        const int r = a.ratio, sh = 3 + (r - 1);  // 8 r = 2^sh
+        const int64_t A = s.p0 + DP_TOK + 127 * r, x = A >> 4;
+        int64_t ic = ((int64_t)(C << (sh + 4)) - A + DP_TOK - 1) >> 4;  // the first unit with C
         ic = ic < 0 ? 0 : ic > m ? m : ic;
         auto G = [&](int64_t v) {
-            const int64_t q = v / M;
-            return M * (q * (q - 1) / 2) + q * (v - q * M);
+            const int64_t q = v >> sh;
+            return ((q * (q - 1) / 2) << sh) + q * (v - (q << sh));
         };
         n = (uint64_t)(G(x + ic) - G(x)) + (uint64_t)(m - ic) * C;
     }
-    return k > last ? n + unit_tiles(a, s, last) : n;
+    return (k > last ? n + unit_tiles(a, s, last) : n) + (uint64_t)k;
 }
 
 // Walks the units of a CTA's share in order.
 struct Walk {
     int b, k, nk;
     SeqQ s;
-    uint32_t t0, t1;  // the unit's tiles in the flattened list
+    uint32_t t0, te;  // the unit's tiles in the list; its last place is te
     __device__ __forceinline__ void start(const DenseArgs& a, const uint32_t* at) {
         b = (int)at[0];
         k = (int)at[1];
         t0 = at[2];
         s = seq_q(a, b, false);
         nk = s.units();
-        t1 = t0 + unit_tiles(a, s, k);
+        te = t0 + unit_tiles(a, s, k);
     }
     __device__ __forceinline__ void next(const DenseArgs& a) {
-        t0 = t1;
+        t0 = te + 1;
         if (++k >= nk) {
             k = 0;
             do {
@@ -142,7 +147,16 @@ struct Walk {
                 nk = s.units();
             } while (nk == 0 && b + 1 < a.B);
         }
-        t1 = t0 + unit_tiles(a, s, k);
+        te = t0 + unit_tiles(a, s, k);
+    }
+    // The first tile at or behind place t, and the end of the CTA's tiles of its unit.
+    // False: there is none before hi.
+    __device__ __forceinline__ bool tiles(const DenseArgs& a, uint32_t& t, uint32_t hi, uint32_t& end) {
+        if (t < hi && t == te) {
+            if (++t < hi) next(a);
+        }
+        end = min(hi, te);
+        return t < hi;
     }
     __device__ __forceinline__ int tokens() const { return min(DP_TOK, s.nq - k * DP_TOK); }
 };
@@ -275,13 +289,13 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's share of the tiles: [lo, hi) of the flattened list ------------
+    // ---- this CTA's share: places [lo, hi) of the list -----------------------------
     const int per_thread = (a.B + DP_THREADS - 1) / DP_THREADS;
     const int b0 = min(a.B, tid * per_thread), b1 = min(a.B, b0 + per_thread);
     uint32_t mine = 0;
     for (int b = b0; b < b1; ++b) {
         const SeqQ s = seq_q(a, b, blockIdx.x == 0);
-        mine += (uint32_t)tiles_before(a, s, s.units());
+        mine += (uint32_t)places_before(a, s, s.units());
     }
     uint32_t total;
     const uint32_t before = block_excl_scan(mine, reinterpret_cast<uint32_t*>(smem + DP_OFF_SCAN), &total);
@@ -291,17 +305,17 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         uint32_t t = before;
         for (int b = b0; b < b1; ++b) {
             const SeqQ s = seq_q(a, b, false);
-            const uint32_t n = (uint32_t)tiles_before(a, s, s.units());
+            const uint32_t n = (uint32_t)places_before(a, s, s.units());
             if (lo < t + n) {
                 int k0 = 0, k1 = s.units();  // the last unit whose first tile is not behind lo
                 while (k1 - k0 > 1) {
                     const int k = (k0 + k1) / 2;
-                    if (tiles_before(a, s, k) <= lo - t) k0 = k;
+                    if (places_before(a, s, k) <= lo - t) k0 = k;
                     else k1 = k;
                 }
                 misc[2] = (uint32_t)b;
                 misc[3] = (uint32_t)k0;
-                misc[4] = t + (uint32_t)tiles_before(a, s, k0);
+                misc[4] = t + (uint32_t)places_before(a, s, k0);
                 break;
             }
             t += n;
@@ -357,8 +371,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             ks ^= 1u;
             kph ^= ks == 0;
         };
-        for (uint32_t t = lo; t < hi;) {
-            const uint32_t end = min(hi, w.t1);
+        for (uint32_t t = lo, end; w.tiles(a, t, hi, end);) {
             const bool two = w.tokens() > DP_TOK / 2;
             wait(&qfull[0], qph);
             qph ^= 1u;
@@ -401,7 +414,6 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     commit(&ofull[1]);
                 }
             }
-            if (t < hi) w.next(a);
         }
         commit(mma_done);
         if (!mbar_wait(mma_done, 0u, kDenseWaitLimit)) *s_timeout = 1;
@@ -465,9 +477,10 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         };
         uint32_t n = 0;  // tiles so far
         Row R[DP_ENT];
-        uint32_t missing;
-        fetch(lo, R, missing);
-        for (uint32_t t = lo; t < hi; ++t, ++n) {
+        uint32_t missing, t = lo, end;
+        bool some = w.tiles(a, t, hi, end);
+        if (some) fetch(t, R, missing);
+        for (; some; ++n) {
             const int s = (int)(n & 1u);
             // A NaN scale of V may not meet a weight of 0 in the product: V becomes 0 there
             // and K NaN, so the tokens that see the entry get NaN and no other.
@@ -509,10 +522,9 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 vcode[i][1] = R[i].v[1];
                 vscale[i] = R[i].vs;
             }
-            if (t + 1 < hi) {  // the next tile's rows, in flight while V is converted
-                if (t + 1 >= w.t1) w.next(a);
-                fetch(t + 1, R, missing);
-            }
+            ++t;  // the next tile's rows, in flight while V is converted
+            some = w.tiles(a, t, hi, end);
+            if (some) fetch(t, R, missing);
             if (n >= 2) wait(&vempty[s], ((n >> 1) - 1) & 1u);
             uint8_t* vt = smem + DP_OFF_V + (size_t)s * DP_TILE;
 #pragma unroll
@@ -529,12 +541,12 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         w.start(a, misc + 2);
         uint32_t sn = 0, units = 0, n = 0;  // S tiles and units of this row tile, tiles of the CTA
         if (tid == 0) {
-            d.cut[2 * blockIdx.x] = lo > w.t0 ? make_int4(w.s.row0 + w.k * DP_TOK, w.tokens(), (int)w.t0, (int)w.t1)
-                                              : make_int4(-1, 0, 0, 0);
+            d.cut[2 * blockIdx.x] = lo > w.t0 && lo < w.te ? make_int4(w.s.row0 + w.k * DP_TOK, w.tokens(), (int)w.t0, (int)w.te)
+                                                           : make_int4(-1, 0, 0, 0);
             d.cut[2 * blockIdx.x + 1] = make_int4((int)lo, 0, 0, 0);
         }
-        for (uint32_t t = lo; t < hi;) {
-            const uint32_t first = t, end = min(hi, w.t1);
+        for (uint32_t t = lo, end; w.tiles(a, t, hi, end);) {
+            const uint32_t first = t;
             const int ntok = w.tokens(), tok = 8 * i + (r >> 4);
             if (8 * i < ntok) {
                 const bool real = tok < ntok;
@@ -544,21 +556,18 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 float c = 1.f;
                 {
                     const uint4* q = reinterpret_cast<const uint4*>(a.q + row * kD);
-                    float f = 0.f, am = 0.f;
-                    if (real) {
+                    uint4 v[4][4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint4 v[4] = {__ldg(q + 4 * x), __ldg(q + 4 * x + 1), __ldg(q + 4 * x + 2), __ldg(q + 4 * x + 3)};
-                            am = fmaxf(am, q_absmax(v));
-                        }
-                    }
-                    q_scale(am, f, c);
+                    for (int x = 0; x < 16; ++x) v[x >> 2][x & 3] = real ? __ldg(q + x) : make_uint4(0, 0, 0, 0);
+                    float f;
+                    q_scale(fmaxf(fmaxf(q_absmax(v[0]), q_absmax(v[1])), fmaxf(q_absmax(v[2]), q_absmax(v[3]))), f, c);
+                    GroupBar{1 + i, 128}.sync();  // the last unit's rows have left the row tile's Q
                     uint8_t* dst = smem + DP_OFF_Q + (size_t)i * DP_TILE + r * 128;
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
-                        const uint4 v = real ? __ldg(q + x) : make_uint4(0, 0, 0, 0);
+                        const uint4 u = v[x >> 2][x & 3];
                         *reinterpret_cast<uint4*>(dst + (size_t)(x >> 3) * DP_HALF + (((x & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(q_half2(v.x, f), q_half2(v.y, f), q_half2(v.z, f), q_half2(v.w, f));
+                            make_uint4(q_half2(u.x, f), q_half2(u.y, f), q_half2(u.z, f), q_half2(u.w, f));
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -666,38 +675,66 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 wait(&ofull[i], units & 1u);
                 ++units;
                 tc_fence_after();
-                const bool whole = first == w.t0 && end == w.t1;
+                const bool whole = first == w.t0 && end == w.te;
                 const int64_t part = (2 * (int64_t)blockIdx.x + (first == w.t0 ? 1 : 0)) * DP_ROWS + 128 * i + r;
+                const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                // A row is a thread's, but a store of 32 rows would touch 32 lines: the warp's rows go
+                // through its share of the row tile's Q (read by now), 16-byte piece p of a row at
+                // p ^ (row & 15), and out 256 bytes of a row at a time.
+                uint8_t* stage = smem + DP_OFF_Q + (size_t)i * DP_TILE + (size_t)(wid & 3) * 8192;
+                const bool bf = whole && a.out_bf16;
+                // the warp's first row, and how many of its 32 there are
+                const int r0 = (wid & 3) * 32, rows = min(32, max(0, ntok * kH - 128 * i - r0));
+                char* to = whole ? static_cast<char*>(a.out) + (row - lane) * kD * (bf ? 2 : 4)
+                                 : reinterpret_cast<char*>(d.part_o + (part - lane) * kD);
 #pragma unroll 1
                 for (int x = 0; x < 4; ++x) {
                     uint32_t v[32];
                     tmem_ld32(tO + 32u * x, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32 && real; e += 8) {
-                        float o[8];
+                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
+                    if (bf) {
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) o[y] = __uint_as_float(v[e + y]);
-                        if (whole) {
-                            dense_store(a, row, 32 * x + e, o, m, l);
-                        } else {
-                            float4* po = reinterpret_cast<float4*>(d.part_o + part * kD + 32 * x + e);
-                            po[0] = make_float4(o[0], o[1], o[2], o[3]);
-                            po[1] = make_float4(o[4], o[5], o[6], o[7]);
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[8 * e + 2 * z]), __uint_as_float(v[8 * e + 2 * z + 1]));
+                                memcpy(&y[z], &b2, 4);
+                            }
+                            *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * x + e) ^ (lane & 15)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4*>(stage + lane * 256 + (((8 * (x & 1) + e) ^ (lane & 15)) << 4)) =
+                                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
-                    __syncwarp();
+                    if (bf ? x == 3 : x & 1) {
+                        __syncwarp();
+                        const int piece = lane & 15;
+                        const int64_t stride = bf ? kD * 2 : kD * 4, at = bf ? 0 : (x >> 1) * 256;
+#pragma unroll 4
+                        for (int y = lane >> 4; y < rows; y += 2)
+                            *reinterpret_cast<uint4*>(to + y * stride + at + piece * 16) =
+                                *reinterpret_cast<const uint4*>(stage + y * 256 + ((piece ^ (y & 15)) << 4));
+                        __syncwarp();
+                    }
                 }
-                if (!whole && real) {
-                    d.part_m[part] = m;
-                    d.part_l[part] = l;
+                if (real) {
+                    if (whole) {
+                        a.lse[row] = l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * 0.6931471805599453f;
+                    } else {
+                        d.part_m[part] = m;
+                        d.part_l[part] = l;
+                    }
                 }
                 tc_fence_before();
             } else {
                 n += end - t;
                 t = end;
             }
-            if (t < hi) w.next(a);
         }
     } else if (tid == 0) {
         d.cut[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -711,45 +748,59 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
     if (tid == 0 && *s_timeout) dev_error(a.err, CSA2_DEV_TIMEOUT);
 }
 
-// Joins the partial results of every unit that spans CTAs: block (c, y) token y
-// of the unit that CTA c continues, if CTA c - 1 began it; one warp per head,
-// sums in a fixed order.
-constexpr int DPJ_THREADS = kH * 32;
+// Joins the partial results of every unit that spans CTAs: block (c, y) tokens
+// 4 y .. 4 y + 3 of the unit that CTA c continues, if CTA c - 1 began it; warp h
+// head h of the four, sums in a fixed order.
+constexpr int DPJ_THREADS = kH * 32, DPJ_TOK = 4;
 __global__ void __launch_bounds__(DPJ_THREADS) dense_prefill_join_kernel(const PrefillDenseArgs d) {
     const int c = blockIdx.x + 1, h = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const int4 cut = d.cut[2 * c];
-    if (cut.x < 0 || (int)blockIdx.y >= cut.y) return;
-    const int per = d.cut[2 * c + 1].x / c;   // CTA c begins at tile c * per
+    const int4 cut = d.cut[2 * c], at = d.cut[2 * c + 1];
+    const int t0 = DPJ_TOK * (int)blockIdx.y;
+    if (cut.x < 0 || t0 >= cut.y) return;
+    const int per = at.x / c;                 // CTA c begins at place c * per
     if (cut.z < (c - 1) * per) return;        // an earlier CTA's block does it
     const int n = (cut.w - 1) / per - c + 2;  // parts
-    const int r = blockIdx.y * kH + h;
-    auto part = [&](int k) { return (int64_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * DP_ROWS + r; };
-    float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, d.part_m[part(k)]);
+    auto part = [&](int k, int y) {
+        return (int64_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * DP_ROWS + (t0 + y) * kH + h;
+    };
+    float M[DPJ_TOK], l[DPJ_TOK];
+    float4 o[DPJ_TOK];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-        const int64_t p = part(k);
-        const float m = d.part_m[p];
-        const float4 v = *reinterpret_cast<const float4*>(d.part_o + p * kD + 4 * lane);
-        const float f = m == -INFINITY ? 0.f : ex2(m - M);
-        o.x += v.x * f;
-        o.y += v.y * f;
-        o.z += v.z * f;
-        o.w += v.w * f;
-        l += d.part_l[p] * f;
+    for (int y = 0; y < DPJ_TOK; ++y) {  // (rows behind the unit's last hold anything; they are not stored)
+        M[y] = -INFINITY;
+        for (int k = lane; k < n; k += 32) M[y] = fmaxf(M[y], d.part_m[part(k, y)]);
+        o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        l[y] = 0.f;
     }
-    // eight dims per storing lane
-    const float4 u = make_float4(__shfl_down_sync(0xffffffffu, o.x, 1), __shfl_down_sync(0xffffffffu, o.y, 1),
-                                 __shfl_down_sync(0xffffffffu, o.z, 1), __shfl_down_sync(0xffffffffu, o.w, 1));
-    if (!(lane & 1)) {
-        const float x[8] = {o.x, o.y, o.z, o.w, u.x, u.y, u.z, u.w};
-        dense_store(d.a, ((int64_t)cut.x + blockIdx.y) * kH + h, 4 * lane, x, M, l);
+#pragma unroll
+    for (int y = 0; y < DPJ_TOK; ++y)
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M[y] = fmaxf(M[y], __shfl_xor_sync(0xffffffffu, M[y], s));
+#pragma unroll 4
+    for (int k = 0; k < n; ++k)
+#pragma unroll
+        for (int y = 0; y < DPJ_TOK; ++y) {
+            const int64_t p = part(k, y);
+            const float m = d.part_m[p];
+            const float4 v = *reinterpret_cast<const float4*>(d.part_o + p * kD + 4 * lane);
+            const float f = m == -INFINITY ? 0.f : ex2(m - M[y]);
+            o[y].x += v.x * f;
+            o[y].y += v.y * f;
+            o[y].z += v.z * f;
+            o[y].w += v.w * f;
+            l[y] += d.part_l[p] * f;
+        }
+#pragma unroll
+    for (int y = 0; y < DPJ_TOK; ++y) {
+        // eight dims per storing lane
+        const float4 u = make_float4(__shfl_down_sync(0xffffffffu, o[y].x, 1), __shfl_down_sync(0xffffffffu, o[y].y, 1),
+                                     __shfl_down_sync(0xffffffffu, o[y].z, 1), __shfl_down_sync(0xffffffffu, o[y].w, 1));
+        if (!(lane & 1) && t0 + y < cut.y) {
+            const float x[8] = {o[y].x, o[y].y, o[y].z, o[y].w, u.x, u.y, u.z, u.w};
+            dense_store(d.a, ((int64_t)cut.x + t0 + y) * kH + h, 4 * lane, x, M[y], l[y]);
+        }
     }
 }
 
@@ -779,14 +830,14 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     d.part_m = d.part_o + (size_t)2 * kDenseCtas * DP_ROWS * kD;
     d.part_l = d.part_m + (size_t)2 * kDenseCtas * DP_ROWS;
     d.cut = reinterpret_cast<int4*>(d.part_l + (size_t)2 * kDenseCtas * DP_ROWS);
-    // tiles there can be: units times the longest sequence's tiles
-    const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS);
+    // places there can be: units times the longest sequence's tiles and one
+    const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS + 1);
     const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);
     LaunchCfg c(dim3(ctas), dim3(DP_THREADS), DP_SMEM, stream);
     e = a.out_bf16 ? cudaLaunchKernelEx(&c.cfg, dense_prefill_kernel<false>, (const PrefillDenseArgs)d)
                    : cudaLaunchKernelEx(&c.cfg, dense_prefill_kernel<true>, (const PrefillDenseArgs)d);
     if (e != cudaSuccess || ctas == 1) return e;
-    LaunchCfg j(dim3(ctas - 1, DP_TOK), dim3(DPJ_THREADS), 0, stream);
+    LaunchCfg j(dim3(ctas - 1, DP_TOK / DPJ_TOK), dim3(DPJ_THREADS), 0, stream);
     return cudaLaunchKernelEx(&j.cfg, dense_prefill_join_kernel, (const PrefillDenseArgs)d);
 }
 
