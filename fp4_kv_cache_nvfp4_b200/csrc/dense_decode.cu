@@ -483,7 +483,6 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
 constexpr int DJ_THREADS = 512;
 __global__ void __launch_bounds__(DJ_THREADS) dense_decode_join_kernel(const DecodeArgs d) {
     __shared__ float4 s_o[16][32];
-    __shared__ float s_l[16];
     const DenseArgs& a = d.a;
     const int c = blockIdx.x + 1, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
@@ -495,36 +494,45 @@ __global__ void __launch_bounds__(DJ_THREADS) dense_decode_join_kernel(const Dec
     const int last = (cut.z - 1) / per, n = last - c + 2;
     const int h = 4 * blockIdx.y + (warp >> 2), w4 = warp & 3;
     auto part = [&](int k) { return (int64_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * kH + h; };
-    float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, d.part_m[part(k)]);
+    // lane k holds the factors of parts k, k + 32, ..., so only the rows are read in the loop
+    constexpr int SLOTS = (kDenseCtas + 31) / 32;
+    float f[SLOTS], pl[SLOTS], M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+        f[s] = lane + 32 * s < n ? d.part_m[part(lane + 32 * s)] : -INFINITY;
+        pl[s] = lane + 32 * s < n ? d.part_l[part(lane + 32 * s)] : 0.f;
+        M = fmaxf(M, f[s]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 8
-    for (int k = w4; k < n; k += 4) {
-        const int64_t p = part(k);
-        const float m = d.part_m[p];
-        const float4 v = *reinterpret_cast<const float4*>(d.part_o + p * kD + 4 * lane);
-        const float f = m == -INFINITY ? 0.f : ex2(m - M);
-        o.x += v.x * f;
-        o.y += v.y * f;
-        o.z += v.z * f;
-        o.w += v.w * f;
-        l += d.part_l[p] * f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+        f[s] = f[s] == -INFINITY ? 0.f : ex2(f[s] - M);
+        l += pl[s] * f[s];
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+#pragma unroll 8
+        for (int k = 32 * s + w4; k < min(n, 32 * s + 32); k += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(d.part_o + part(k) * kD + 4 * lane);
+            const float g = __shfl_sync(0xffffffffu, f[s], k & 31);
+            o.x += v.x * g;
+            o.y += v.y * g;
+            o.z += v.z * g;
+            o.w += v.w * g;
+        }
     s_o[warp][lane] = o;
-    if (lane == 0) s_l[warp] = l;
     __syncthreads();
     if (w4 == 0 && lane < 16) {
         float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        l = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const float4 x = s_o[warp + w][2 * lane], y = s_o[warp + w][2 * lane + 1];
             r[0] += x.x, r[1] += x.y, r[2] += x.z, r[3] += x.w;
             r[4] += y.x, r[5] += y.y, r[6] += y.z, r[7] += y.w;
-            l += s_l[warp + w];
         }
         dense_store(a, (int64_t)cut.x * kH + h, 8 * lane, r, M, l);
     }

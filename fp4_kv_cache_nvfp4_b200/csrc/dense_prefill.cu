@@ -48,7 +48,8 @@ constexpr size_t DP_OFF_Q = 0;                            // [2 row tiles]
 constexpr size_t DP_OFF_K = DP_OFF_Q + 2 * DP_TILE;       // [2 slots]
 constexpr size_t DP_OFF_V = DP_OFF_K + 2 * DP_TILE;       // [2 slots]
 constexpr size_t DP_OFF_OK = DP_OFF_V + 2 * DP_TILE;      // [4][16 B]: one bit per entry of a K tile, 0: missing page
-constexpr size_t DP_OFF_BAR = DP_OFF_OK + 64;
+constexpr size_t DP_OFF_ML = DP_OFF_OK + 64;              // [128] (m, l) of the second group's rows
+constexpr size_t DP_OFF_BAR = DP_OFF_ML + 1024;
 constexpr int DP_NBAR = 4 * 2 + 4 * 2 + 1;
 constexpr size_t DP_OFF_SCAN = DP_OFF_BAR + DP_NBAR * 8;  // [64] words
 constexpr size_t DP_OFF_MISC = DP_OFF_SCAN + 256;         // tmem base, timeout flag, start sequence, unit, its first tile
@@ -159,6 +160,12 @@ struct Walk {
         return t < hi;
     }
     __device__ __forceinline__ int tokens() const { return min(DP_TOK, s.nq - k * DP_TOK); }
+    // A unit of one row tile: the two groups of softmax warps take its entry tiles in
+    // turn, each with its own O, and join them at the end.
+    template <bool PAIRED>
+    __device__ __forceinline__ bool split(uint32_t t, uint32_t end) const {
+        return PAIRED && tokens() <= DP_TOK / 2 && end - t >= 2;
+    }
 };
 
 // ---- tensor-core helpers --------------------------------------------------------------
@@ -244,8 +251,9 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// SPLIT: P as two fp16 terms (fp32 results)
-template <bool SPLIT>
+// SPLIT: P as two fp16 terms (fp32 results).  PAIRED: units of one row tile use
+// both groups of softmax warps.
+template <bool SPLIT, bool PAIRED>
 __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const PrefillDenseArgs d) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -339,9 +347,9 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         uint32_t ks = 0, kph = 0, vs = 0, vph = 0, qph = 0, qph1 = 0, pph0 = 0, pph1 = 0;  // slots and phases
         const uint32_t qlo = desc_lo(smem_u32(smem + DP_OFF_Q)), klo = desc_lo(smem_u32(smem + DP_OFF_K)),
                        vlo = desc_lo_mn(smem_u32(smem + DP_OFF_V));
-        auto mma_s = [&](int i) {  // S of row tile i over the K tile in slot ks
+        auto mma_s = [&](int i, int qi) {  // S i: row tile qi over the K tile in slot ks
             if (leader) {
-                const uint32_t q = qlo + (uint32_t)i * (DP_TILE >> 4), k = klo + ks * (DP_TILE >> 4);
+                const uint32_t q = qlo + (uint32_t)qi * (DP_TILE >> 4), k = klo + ks * (DP_TILE >> 4);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const uint32_t o = (uint32_t)(x >> 2) * (DP_HALF >> 4) + 2u * (x & 3);
@@ -375,14 +383,46 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             const bool two = w.tokens() > DP_TOK / 2;
             wait(&qfull[0], qph);
             qph ^= 1u;
+            if (w.split<PAIRED>(t, end)) {
+                const uint32_t first = t;
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    wait(&kfull[ks], kph);
+                    tc_fence_after();
+                    mma_s(i, 0);
+                    next_k();
+                }
+#pragma unroll 1
+                for (; t < end; ++t) {
+                    const int i = (int)(t - first) & 1;
+                    wait(&vfull[vs], vph);
+                    wait(&pfull[i], i ? pph1 : pph0);
+                    if (i) pph1 ^= 1u;
+                    else pph0 ^= 1u;
+                    tc_fence_after();
+                    mma_pv(i, t - first < 2);
+                    commit(&vempty[vs]);
+                    vs ^= 1u;
+                    vph ^= vs == 0;
+                    if (t + 2 < end) {
+                        wait(&kfull[ks], kph);
+                        tc_fence_after();
+                        mma_s(i, 0);
+                        next_k();
+                    } else {
+                        commit(&ofull[i]);
+                    }
+                }
+                continue;
+            }
             if (two) {
                 wait(&qfull[1], qph1);
                 qph1 ^= 1u;
             }
             wait(&kfull[ks], kph);
             tc_fence_after();
-            mma_s(0);
-            if (two) mma_s(1);
+            mma_s(0, 0);
+            if (two) mma_s(1, 1);
             next_k();
             for (const uint32_t first = t; t < end; ++t) {
                 const bool more = t + 1 < end;
@@ -394,7 +434,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 if (more) {
                     wait(&kfull[ks], kph);
                     tc_fence_after();
-                    mma_s(0);
+                    mma_s(0, 0);
                 } else {
                     commit(&ofull[0]);
                 }
@@ -408,7 +448,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 vs ^= 1u;
                 vph ^= vs == 0;
                 if (more) {
-                    if (two) mma_s(1);
+                    if (two) mma_s(1, 1);
                     next_k();
                 } else if (two) {
                     commit(&ofull[1]);
@@ -547,8 +587,9 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         }
         for (uint32_t t = lo, end; w.tiles(a, t, hi, end);) {
             const uint32_t first = t;
-            const int ntok = w.tokens(), tok = 8 * i + (r >> 4);
-            if (8 * i < ntok) {
+            const bool split = w.split<PAIRED>(t, end);
+            const int qi = split ? 0 : i, ntok = w.tokens(), tok = 8 * qi + (r >> 4);
+            if (8 * qi < ntok) {
                 const bool real = tok < ntok;
                 const int64_t row = ((int64_t)w.s.row0 + w.k * DP_TOK + tok) * kH + (r & 15);
                 const int seen = real ? seen_by(a, w.s, w.k * DP_TOK + tok) : 0;
@@ -562,19 +603,25 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     float f;
                     q_scale(fmaxf(fmaxf(q_absmax(v[0]), q_absmax(v[1])), fmaxf(q_absmax(v[2]), q_absmax(v[3]))), f, c);
                     GroupBar{1 + i, 128}.sync();  // the last unit's rows have left the row tile's Q
-                    uint8_t* dst = smem + DP_OFF_Q + (size_t)i * DP_TILE + r * 128;
+                    uint8_t* dst = smem + DP_OFF_Q + (size_t)qi * DP_TILE + r * 128;
+                    const bool mine = !split || i == 0;  // (the other group only needs c)
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
+                    for (int x = 0; x < 16 && mine; ++x) {
                         const uint4 u = v[x >> 2][x & 3];
                         *reinterpret_cast<uint4*>(dst + (size_t)(x >> 3) * DP_HALF + (((x & 7) ^ (r & 7)) << 4)) =
                             make_uint4(q_half2(u.x, f), q_half2(u.y, f), q_half2(u.z, f), q_half2(u.w, f));
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&qfull[i]);
+                    if (lane == 0 && mine) mbar_arrive(&qfull[i]);
                 }
                 float m = -INFINITY, bias = kPBias, l = 0.f;
-                for (; t < end; ++t, ++n, ++sn) {
+                const uint32_t step = split ? 2u : 1u, n_end = n + (end - t);
+                if (split) {
+                    t += (uint32_t)i;
+                    n += (uint32_t)i;
+                }
+                for (; t < end; t += step, n += step, ++sn) {
                     wait(&sfull[i], sn & 1u);
                     tc_fence_after();
                     const int nv = seen - (int)(t - w.t0) * DP_KEYS;  // entries of the tile this row sees
@@ -628,7 +675,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                                     tmem_st16(tS + y, p);
                                 }
                             }
-                            if (t > first) {  // O is complete: S of this tile was issued after its last product
+                            if (t - first >= step) {  // O is complete: S of this tile was issued after its last product
 #pragma unroll 1
                                 for (int y = 0; y < 128; y += 16) {
                                     uint32_t o[16];
@@ -671,20 +718,55 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&pfull[i]);
                 }
+                t = end;
+                n = n_end;
                 // ---- the unit's rows ---------------------------------------------------------------
                 wait(&ofull[i], units & 1u);
                 ++units;
                 tc_fence_after();
                 const bool whole = first == w.t0 && end == w.te;
-                const int64_t part = (2 * (int64_t)blockIdx.x + (first == w.t0 ? 1 : 0)) * DP_ROWS + 128 * i + r;
+                const int64_t part = (2 * (int64_t)blockIdx.x + (first == w.t0 ? 1 : 0)) * DP_ROWS + 128 * qi + r;
+                // This thread's piece p (16 bytes) of its row's 64-dim half hf on the way through
+                // shared memory: the row tiles' Q, read by now.  8 KiB a warp, 16 where the two
+                // groups join (a half each, so that it lies where the second group left its O).
+                uint8_t* const stage = smem + DP_OFF_Q + (split ? (size_t)(wid & 3) * 16384 : (size_t)i * DP_TILE + (size_t)(wid & 3) * 8192);
+                auto piece_at = [&](int hf, int p) { return reinterpret_cast<uint4*>(stage + (split ? hf * 8192 : 0) + lane * 256 + ((p ^ (lane & 15)) << 4)); };
+                float f0 = 1.f, f1 = 0.f;  // factors of this group's O and the other's
+                if (split) {
+                    float2* ml = reinterpret_cast<float2*>(smem + DP_OFF_ML) + r;
+                    if (i == 1) {
+                        *ml = make_float2(m, l);
+#pragma unroll 1
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t v[32];
+                            tmem_ld32(tO + 32u * x, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *piece_at(x >> 1, 8 * (x & 1) + e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        }
+                        tc_fence_before();
+                    }
+                    GroupBar{3, 256}.sync();
+                    if (i == 1) {
+                        GroupBar{3, 256}.sync();  // the first group has read it, and is done with the row tiles' Q
+                        continue;
+                    }
+                    const float m1 = ml->x, M = fmaxf(m, m1);
+                    f0 = m == -INFINITY ? 0.f : ex2(m - M);
+                    f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+                    l = (m == -INFINITY ? l : l * f0) + (m1 == -INFINITY ? ml->y : ml->y * f1);  // (a NaN sum stays one)
+                    m = M;
+                }
                 const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                f0 *= inv;
+                f1 *= inv;
                 // A row is a thread's, but a store of 32 rows would touch 32 lines: the warp's rows go
                 // through its share of the row tile's Q (read by now), 16-byte piece p of a row at
                 // p ^ (row & 15), and out 256 bytes of a row at a time.
-                uint8_t* stage = smem + DP_OFF_Q + (size_t)i * DP_TILE + (size_t)(wid & 3) * 8192;
                 const bool bf = whole && a.out_bf16;
                 // the warp's first row, and how many of its 32 there are
-                const int r0 = (wid & 3) * 32, rows = min(32, max(0, ntok * kH - 128 * i - r0));
+                const int r0 = (wid & 3) * 32, rows = min(32, max(0, ntok * kH - 128 * qi - r0));
                 char* to = whole ? static_cast<char*>(a.out) + (row - lane) * kD * (bf ? 2 : 4)
                                  : reinterpret_cast<char*>(d.part_o + (part - lane) * kD);
 #pragma unroll 1
@@ -693,7 +775,17 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     tmem_ld32(tO + 32u * x, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
+                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
+                    if (split) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 u = *piece_at(x >> 1, 8 * (x & 1) + e);
+                            v[4 * e] = __float_as_uint(fmaf(__uint_as_float(u.x), f1, __uint_as_float(v[4 * e])));
+                            v[4 * e + 1] = __float_as_uint(fmaf(__uint_as_float(u.y), f1, __uint_as_float(v[4 * e + 1])));
+                            v[4 * e + 2] = __float_as_uint(fmaf(__uint_as_float(u.z), f1, __uint_as_float(v[4 * e + 2])));
+                            v[4 * e + 3] = __float_as_uint(fmaf(__uint_as_float(u.w), f1, __uint_as_float(v[4 * e + 3])));
+                        }
+                    }
                     if (bf) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -703,13 +795,12 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                                 const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[8 * e + 2 * z]), __uint_as_float(v[8 * e + 2 * z + 1]));
                                 memcpy(&y[z], &b2, 4);
                             }
-                            *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * x + e) ^ (lane & 15)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *piece_at(0, 4 * x + e) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(stage + lane * 256 + (((8 * (x & 1) + e) ^ (lane & 15)) << 4)) =
-                                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                            *piece_at(x >> 1, 8 * (x & 1) + e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                     if (bf ? x == 3 : x & 1) {
                         __syncwarp();
@@ -718,7 +809,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
 #pragma unroll 4
                         for (int y = lane >> 4; y < rows; y += 2)
                             *reinterpret_cast<uint4*>(to + y * stride + at + piece * 16) =
-                                *reinterpret_cast<const uint4*>(stage + y * 256 + ((piece ^ (y & 15)) << 4));
+                                *reinterpret_cast<const uint4*>(stage + (split && !bf ? (x >> 1) * 8192 : 0) + y * 256 + ((piece ^ (y & 15)) << 4));
                         __syncwarp();
                     }
                 }
@@ -731,6 +822,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     }
                 }
                 tc_fence_before();
+                if (split) GroupBar{3, 256}.sync();
             } else {
                 n += end - t;
                 t = end;
@@ -749,9 +841,10 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
 }
 
 // Joins the partial results of every unit that spans CTAs: block (c, y) tokens
-// 4 y .. 4 y + 3 of the unit that CTA c continues, if CTA c - 1 began it; warp h
-// head h of the four, sums in a fixed order.
-constexpr int DPJ_THREADS = kH * 32, DPJ_TOK = 4;
+// 2 y and 2 y + 1 of the unit that CTA c continues, if CTA c - 1 began it; warp h
+// head h of both, sums in a fixed order.  Lane k holds the factors of parts k,
+// k + 32, ..., so only the rows themselves are read in the loop, eight at a time.
+constexpr int DPJ_THREADS = kH * 32, DPJ_TOK = 2, DPJ_SLOTS = (kDenseCtas + 31) / 32;
 __global__ void __launch_bounds__(DPJ_THREADS) dense_prefill_join_kernel(const PrefillDenseArgs d) {
     const int c = blockIdx.x + 1, h = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
@@ -765,33 +858,43 @@ __global__ void __launch_bounds__(DPJ_THREADS) dense_prefill_join_kernel(const P
     auto part = [&](int k, int y) {
         return (int64_t)(k == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + k)) * DP_ROWS + (t0 + y) * kH + h;
     };
-    float M[DPJ_TOK], l[DPJ_TOK];
+    float f[DPJ_TOK][DPJ_SLOTS], M[DPJ_TOK], l[DPJ_TOK];
     float4 o[DPJ_TOK];
 #pragma unroll
-    for (int y = 0; y < DPJ_TOK; ++y) {  // (rows behind the unit's last hold anything; they are not stored)
+    for (int y = 0; y < DPJ_TOK; ++y) {  // (a row behind the unit's last holds anything; it is not stored)
+        float pl[DPJ_SLOTS];
         M[y] = -INFINITY;
-        for (int k = lane; k < n; k += 32) M[y] = fmaxf(M[y], d.part_m[part(k, y)]);
-        o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-        l[y] = 0.f;
-    }
 #pragma unroll
-    for (int y = 0; y < DPJ_TOK; ++y)
+        for (int s = 0; s < DPJ_SLOTS; ++s) {
+            f[y][s] = lane + 32 * s < n ? d.part_m[part(lane + 32 * s, y)] : -INFINITY;
+            pl[s] = lane + 32 * s < n ? d.part_l[part(lane + 32 * s, y)] : 0.f;
+            M[y] = fmaxf(M[y], f[y][s]);
+        }
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) M[y] = fmaxf(M[y], __shfl_xor_sync(0xffffffffu, M[y], s));
-#pragma unroll 4
-    for (int k = 0; k < n; ++k)
+        l[y] = 0.f;
 #pragma unroll
-        for (int y = 0; y < DPJ_TOK; ++y) {
-            const int64_t p = part(k, y);
-            const float m = d.part_m[p];
-            const float4 v = *reinterpret_cast<const float4*>(d.part_o + p * kD + 4 * lane);
-            const float f = m == -INFINITY ? 0.f : ex2(m - M[y]);
-            o[y].x += v.x * f;
-            o[y].y += v.y * f;
-            o[y].z += v.z * f;
-            o[y].w += v.w * f;
-            l[y] += d.part_l[p] * f;
+        for (int s = 0; s < DPJ_SLOTS; ++s) {
+            f[y][s] = f[y][s] == -INFINITY ? 0.f : ex2(f[y][s] - M[y]);
+            l[y] += pl[s] * f[y][s];
         }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) l[y] += __shfl_xor_sync(0xffffffffu, l[y], s);
+        o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int s = 0; s < DPJ_SLOTS; ++s)
+#pragma unroll 8
+        for (int k = 32 * s; k < min(n, 32 * s + 32); ++k)
+#pragma unroll
+            for (int y = 0; y < DPJ_TOK; ++y) {
+                const float4 v = *reinterpret_cast<const float4*>(d.part_o + part(k, y) * kD + 4 * lane);
+                const float g = __shfl_sync(0xffffffffu, f[y][s], k & 31);
+                o[y].x += v.x * g;
+                o[y].y += v.y * g;
+                o[y].z += v.z * g;
+                o[y].w += v.w * g;
+            }
 #pragma unroll
     for (int y = 0; y < DPJ_TOK; ++y) {
         // eight dims per storing lane
@@ -816,7 +919,8 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!init[dev]) {
-        for (const void* k : {(const void*)dense_prefill_kernel<false>, (const void*)dense_prefill_kernel<true>}) {
+        for (const void* k : {(const void*)dense_prefill_kernel<false, false>, (const void*)dense_prefill_kernel<true, false>,
+                              (const void*)dense_prefill_kernel<false, true>, (const void*)dense_prefill_kernel<true, true>}) {
             e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DP_SMEM);
             if (e != cudaSuccess) return e;
         }
@@ -834,8 +938,11 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS + 1);
     const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);
     LaunchCfg c(dim3(ctas), dim3(DP_THREADS), DP_SMEM, stream);
-    e = a.out_bf16 ? cudaLaunchKernelEx(&c.cfg, dense_prefill_kernel<false>, (const PrefillDenseArgs)d)
-                   : cudaLaunchKernelEx(&c.cfg, dense_prefill_kernel<true>, (const PrefillDenseArgs)d);
+    // PAIRED_MEASURED
+    const bool paired = a.T <= DP_TOK / 2 * (int64_t)a.B;
+    auto kernel = a.out_bf16 ? (paired ? dense_prefill_kernel<false, true> : dense_prefill_kernel<false, false>)
+                             : (paired ? dense_prefill_kernel<true, true> : dense_prefill_kernel<true, false>);
+    e = cudaLaunchKernelEx(&c.cfg, kernel, (const PrefillDenseArgs)d);
     if (e != cudaSuccess || ctas == 1) return e;
     LaunchCfg j(dim3(ctas - 1, DP_TOK / DPJ_TOK), dim3(DPJ_THREADS), 0, stream);
     return cudaLaunchKernelEx(&j.cfg, dense_prefill_join_kernel, (const PrefillDenseArgs)d);

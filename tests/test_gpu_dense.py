@@ -162,6 +162,30 @@ def test_prefill(csa2, page, lens, ns, causal, ratio, dtype):
             check(out[r], lse[r], reference(q[r], c.rows(b), seen), f"seq {b} ({n} over {L})")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,n,L", [(3, 5, 9000), (200, 2, 300), (4, 8, 1290), (2, 9, 2000)])
+def test_prefill_drafts(csa2, B, n, L, dtype):
+    """A few tokens each over long sequences (units of one row tile, over several CTAs or
+    many to a CTA), a missing page and a rising maximum among them."""
+    lens = [L - 37 * (b % 5) for b in range(B)]
+    c = DenseCase(csa2, lens, 64, seed=B)
+    sl = c.slots(1, lens[1])
+    rise = torch.linspace(0.05, 60, lens[1]).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.scales[sl[:, None], torch.arange(8)] = rise[:, None].expand(lens[1], 8)
+    pages = c.table.clone()
+    c.table[0, 2] = -1
+    c.upload()
+    q = queries(B * n, seed=B)
+    start = [x - n for x in lens]
+    out, lse, err = prefill(csa2, c, q, [n * b for b in range(B + 1)], DT[dtype], start)
+    assert err == DEV_PAGE
+    c.table = pages
+    for b in [0, 1, B - 1]:
+        r = slice(n * b, n * b + n)
+        check(out[r], lse[r], reference(q[r], c.rows(b), seen_of(lens[b], n, start[b], 1),
+                                        range(128, 192) if b == 0 else None), f"seq {b}")
+
+
 def test_prefill_rows_of_no_sequence_stay(csa2):
     """Rows before cu_q[0], of a range that is not ascending or leaves T, and
     behind the last sequence are left as they were; early tokens of a ratio-2
