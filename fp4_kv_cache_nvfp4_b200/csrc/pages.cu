@@ -37,28 +37,33 @@ struct PageCaches {
     int n, page_size;
 };
 
-// Copies one physical page of one array, 16 bytes per thread and load, four
-// loads in flight.
-__device__ __forceinline__ void copy_plane(uint8_t* base, int64_t bytes, int32_t src, int32_t dst) {
-    const uint4* s = reinterpret_cast<const uint4*>(base + bytes * src);
-    uint4* d = reinterpret_cast<uint4*>(base + bytes * dst);
-    const int n = (int)(bytes >> 4);
-    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * PG_COPY_THREADS) {
-        uint4 v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (i0 + u * PG_COPY_THREADS < n) v[u] = s[i0 + u * PG_COPY_THREADS];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (i0 + u * PG_COPY_THREADS < n) d[i0 + u * PG_COPY_THREADS] = v[u];
-    }
-}
+// Copies a physical page in every array of cache c.  Its 16-byte pieces (18 per
+// entry: codes 8, indexer K 8, scales 1, pooled indexer K 1) are one index space,
+// so that a page of 64 entries is one round of five loads in flight per thread, not
+// one latency per array.
 __device__ __forceinline__ void copy_page(const PageCaches& p, int c, int32_t src, int32_t dst) {
-    copy_plane(p.codes[c], (int64_t)p.page_size * kCodeBytes, src, dst);
-    copy_plane(p.scales[c], (int64_t)p.page_size * kScales, src, dst);
-    if (p.idx[c]) copy_plane(reinterpret_cast<uint8_t*>(p.idx[c]), (int64_t)p.page_size * kID * 2, src, dst);
-    if (p.pooled[c])
-        copy_plane(reinterpret_cast<uint8_t*>(p.pooled[c]), (int64_t)p.page_size / kBlk * kID * 2, src, dst);
+    const int ps = p.page_size, n = ps * (p.idx[c] ? (p.pooled[c] ? 18 : 17) : 9);
+    auto piece = [&](int i, int32_t page) -> uint4* {
+        uint8_t* base = p.codes[c];
+        int per = 8 * ps;
+        if (i >= per) {
+            i -= per;
+            if (i < ps) base = p.scales[c], per = ps;
+            else if ((i -= ps) < per) base = reinterpret_cast<uint8_t*>(p.idx[c]);
+            else i -= per, base = reinterpret_cast<uint8_t*>(p.pooled[c]), per = ps;
+        }
+        return reinterpret_cast<uint4*>(base) + (int64_t)per * page + i;
+    };
+    constexpr int U = 5;
+    for (int i0 = threadIdx.x; i0 < n; i0 += U * PG_COPY_THREADS) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * PG_COPY_THREADS < n) v[u] = *piece(i0 + u * PG_COPY_THREADS, src);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * PG_COPY_THREADS < n) *piece(i0 + u * PG_COPY_THREADS, dst) = v[u];
+    }
 }
 
 // ---- copy: pairs of pages -----------------------------------------------------
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(PG_SCAN_THREADS) fork_count_kernel(ForkArgs a)
 // the requests and ranks those that need a page.
 __global__ void __launch_bounds__(PG_SCAN_THREADS) fork_list_kernel(ForkArgs a) {
     __shared__ uint32_t tmp[64];
-    __shared__ int32_t s_child[kMaxForks], s_parent[kMaxForks];
+    __shared__ __align__(16) int32_t s_child[kMaxForks], s_parent[kMaxForks];
     const int tid = threadIdx.x, chunks = (int)gridDim.x - 1;
     pdl_wait();
     pdl_trigger();
@@ -156,9 +161,9 @@ __global__ void __launch_bounds__(PG_SCAN_THREADS) fork_list_kernel(ForkArgs a) 
         if ((int)blockIdx.x + 1 == chunks && tid == 0) *a.n_free = (int)(before + total);
         return;
     }
-    if (tid < a.n) {
-        s_child[tid] = a.children[tid];
-        s_parent[tid] = a.parents[tid];
+    if (tid < kMaxForks) {
+        s_child[tid] = tid < a.n ? a.children[tid] : -1;
+        s_parent[tid] = tid < a.n ? a.parents[tid] : -1;
     }
     __syncthreads();
     ForkPlan pl{-1, -1, 0, -1};
@@ -171,7 +176,11 @@ __global__ void __launch_bounds__(PG_SCAN_THREADS) fork_list_kernel(ForkArgs a) 
             dev_error(a.err, CSA2_DEV_SLOT);
         } else {
             bool taken = a.lens[c] != 0;  // the row is in use
-            for (int j = 0; j < a.n; ++j) taken |= (j < tid && s_child[j] == c) || s_parent[j] == c;
+            for (int j = 0; j < a.n; j += 4) {  // (behind the last request both are -1)
+                const int4 x = *reinterpret_cast<const int4*>(s_child + j), y = *reinterpret_cast<const int4*>(s_parent + j);
+                taken |= (x.x == c && j < tid) || (x.y == c && j + 1 < tid) || (x.z == c && j + 2 < tid) ||
+                         (x.w == c && j + 3 < tid) || y.x == c || y.y == c || y.z == c || y.w == c;
+            }
             const int32_t len = a.lens[f];
             if (taken) {
                 dev_error(a.err, CSA2_DEV_SLOT);
