@@ -394,6 +394,14 @@ def kv_pages_workspace_bytes(n_phys_pages: int, n: int = 0) -> int:
     return size
 
 
+def _mapped(caches) -> None:
+    """Every array of the caches is where kernels can write it."""
+    for c in caches:
+        for t in (c.codes, c.scales, c.idx_k, c.pooled):
+            if t is not None and not t.is_cuda and not t.is_pinned():
+                raise ValueError(f"a cache's array is on {t.device} and not pinned")
+
+
 def _page_args(caches, refs, seq_lens, err):
     """The caches as a C array, their common table and the device."""
     if not caches:
@@ -401,6 +409,7 @@ def _page_args(caches, refs, seq_lens, err):
     c0 = caches[0]
     table = c0.page_table
     dev = _device(table)
+    _mapped(caches)
     for c in caches[1:]:
         if c.page_table.data_ptr() != table.data_ptr() or c.page_table.shape != table.shape:
             raise ValueError("caches: they do not share one page table")
@@ -416,6 +425,7 @@ def kv_pages_copy(caches: list[KVCache], src, dst, err=None, stream=None) -> Non
     if not caches:
         raise ValueError("caches: empty")
     dev = _device(src)
+    _mapped(caches)
     _on_gpu("src", src, _I32T, (None,), dev)
     _on_gpu("dst", dst, _I32T, (src.numel(),), dev)
     _on_gpu("err", err, _I32T, (1,), dev, optional=True)

@@ -938,7 +938,10 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS + 1);
     const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);
     LaunchCfg c(dim3(ctas), dim3(DP_THREADS), DP_SMEM, stream);
-    // PAIRED_MEASURED
+    // By the average tokens of a sequence (cu_q is on the device): at most one row
+    // tile's take the paired kernel.  Measured, paired / not: 8 x 5 tokens over 65,536
+    // entries 77.0 / 83.4 us, 8 x 5 over 32,768 50.2 / 52.1; 4096 tokens over 16,384
+    // entries 497 / 485 us.
     const bool paired = a.T <= DP_TOK / 2 * (int64_t)a.B;
     auto kernel = a.out_bf16 ? (paired ? dense_prefill_kernel<false, true> : dense_prefill_kernel<false, false>)
                              : (paired ? dense_prefill_kernel<true, true> : dense_prefill_kernel<true, false>);

@@ -26,8 +26,10 @@ constexpr int PG_SCAN_THREADS = 1024;   // four counts per thread
 constexpr int PG_COPY_THREADS = 256;
 // Up to this many chunks every CTA counts the chunks before its own (and, to
 // compact, all) itself from L2; above, a kernel counts each chunk once first.
-// COUNTS_MEASURED
-constexpr int PG_SELF_COUNT = 16;
+// Measured, compact with little to move, counting itself / by a kernel: 255
+// pages 10.6 / 11.9 us, 12,000 pages 12.6 / 13.4, 60,000 pages 14.7 / 12.9,
+// 240,000 pages 27.5 / 13.3.
+constexpr int PG_SELF_COUNT = 6;
 
 struct PageCaches {
     uint8_t* codes[kMaxCaches];
