@@ -39,11 +39,16 @@ constexpr uint32_t DD_MIN_SHARE = 4;             // chunks per CTA at least
 constexpr int DD_STAGES = 2;                     // chunks of a warp's ring
 constexpr int DD_CODES = DD_CHUNK * kCodeBytes;  // 8 KiB per stage
 constexpr int DD_SCALES = DD_CHUNK * kScales;    // 1 KiB
+// The tensor core's fp32 sums drop bits at every product, towards zero: an fp32
+// result's O moves to shared memory, where it is added with rounding, after so many
+// chunks (32 products of a tile).  Relative error at 1M entries 2.0e-6 without, 0.6e-6 with
+// (70 us instead of 63; after two chunks 0.4e-6, 77 us).
+constexpr uint32_t DD_DRAIN = 4;
 constexpr int DD_OROW = kD + 4;                  // floats per row of the joining slab (bank spread)
 constexpr size_t DD_OFF_CODES = 0;               // [warps][stages]
 constexpr size_t DD_OFF_SCALES = DD_OFF_CODES + (size_t)DD_WARPS * DD_STAGES * DD_CODES;
-constexpr size_t DD_OFF_SLAB = DD_OFF_SCALES + (size_t)DD_WARPS * DD_STAGES * DD_SCALES;  // [warps / 2][16][DD_OROW] floats
-constexpr size_t DD_OFF_M = DD_OFF_SLAB + (size_t)DD_WARPS / 2 * kH * DD_OROW * 4;        // [warps][16]
+constexpr size_t DD_OFF_SLAB = DD_OFF_SCALES + (size_t)DD_WARPS * DD_STAGES * DD_SCALES;  // [warps][16][DD_OROW] floats
+constexpr size_t DD_OFF_M = DD_OFF_SLAB + (size_t)DD_WARPS * kH * DD_OROW * 4;            // [warps][16]
 constexpr size_t DD_OFF_L = DD_OFF_M + DD_WARPS * kH * 4;                                 // [warps][16]
 constexpr size_t DD_OFF_BAR = DD_OFF_L + DD_WARPS * kH * 4;                               // [warps][stages]
 constexpr size_t DD_OFF_MISC = DD_OFF_BAR + DD_WARPS * DD_STAGES * 8;
@@ -219,7 +224,39 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
 
+            // this warp's rows of the slab: heads g and g + 8; columns 2 t and 2 t + 1 of tile i
+            // are dims 32 t + i and 32 t + 16 + i
+            float* my = slab + ((size_t)warp * kH + g) * DD_OROW + 32 * t4;
+            // O over f0 and f1, plus what the slab holds (times s0, s1) if `add`
+            auto to_slab = [&](float f0, float f1, bool add, float s0, float s1) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float4* at = reinterpret_cast<float4*>(my + (e >> 1) * 8 * DD_OROW + (e & 1) * 16 + i);
+                        const float f = e < 2 ? f0 : f1, sc = e < 2 ? s0 : s1;
+                        float4 v = make_float4(O[i][e] * f, O[i + 1][e] * f, O[i + 2][e] * f, O[i + 3][e] * f);
+                        if (add) {
+                            const float4 u = *at;
+                            v = make_float4(fmaf(u.x, sc, v.x), fmaf(u.y, sc, v.y), fmaf(u.z, sc, v.z), fmaf(u.w, sc, v.w));
+                        }
+                        *at = v;
+                    }
+            };
+            auto ratio = [](float from, float to) { return from == -INFINITY ? 0.f : ex2(from - to); };
+            float d0 = -INFINITY, d1 = -INFINITY;  // the maxima that the slab's sums are over (fp32 results)
+            bool drained = false;
+            uint32_t held = 0;                     // chunks in O
+
             for (; c < seg1; c += DD_WARPS, ++done) {
+                if (SPLIT && held++ == DD_DRAIN) {
+                    held = 1;
+                    to_slab(1.f, 1.f, drained, ratio(d0, m0), ratio(d1, m1));
+                    drained = true;
+                    d0 = m0, d1 = m1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
+                }
                 const int st = (int)(done & 1u);
                 if (!mbar_wait(&full[st], (done >> 1) & 1u, kDenseWaitLimit)) {  // give up: no copy stays in flight
                     if (c_next - c > DD_WARPS) mbar_wait(&full[st ^ 1], ((done + 1) >> 1) & 1u, kDenseWaitLimit);
@@ -402,36 +439,8 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                 M0 = fmaxf(M0, wm[w * kH + g]);
                 M1 = fmaxf(M1, wm[w * kH + g + 8]);
             }
-            const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                O[i][0] *= f0;
-                O[i][1] *= f0;
-                O[i][2] *= f1;
-                O[i][3] *= f1;
-            }
-            // columns 2 t and 2 t + 1 of tile i are dims 32 t + i and 32 t + 16 + i;
-            // the upper half of the warps writes its rows, the lower half adds its own
-            constexpr int HALF = DD_WARPS / 2;
-            float* my = slab + ((size_t)(warp % HALF) * kH + g) * DD_OROW + 32 * t4;
-#pragma unroll
-            for (int pass = 0; pass < 2; ++pass) {
-                if ((warp < HALF) == (pass == 1)) {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float4* at = reinterpret_cast<float4*>(my + (e >> 1) * 8 * DD_OROW + (e & 1) * 16 + i);
-                            float4 v = make_float4(O[i][e], O[i + 1][e], O[i + 2][e], O[i + 3][e]);
-                            if (pass == 1) {
-                                const float4 u = *at;
-                                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-                            }
-                            *at = v;
-                        }
-                }
-                __syncthreads();
-            }
+            to_slab(ratio(m0, M0), ratio(m1, M1), SPLIT && drained, ratio(d0, M0), ratio(d1, M1));
+            __syncthreads();
             if (tid < kH * 16) {
                 const int h = tid >> 4, d8 = (tid & 15) * 8;  // 16 heads x 16 threads of 8 dims
                 float M = -INFINITY, l = 0.f, o[8];
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                     if (mw != -INFINITY) l += wl[w * kH + h] * ex2(mw - M);
                 }
 #pragma unroll
-                for (int w = 0; w < HALF; ++w) {
+                for (int w = 0; w < DD_WARPS; ++w) {
                     const float* p = slab + ((size_t)w * kH + h) * DD_OROW + d8;
                     const float4 v0 = *reinterpret_cast<const float4*>(p), v1 = *reinterpret_cast<const float4*>(p + 4);
                     o[0] += v0.x, o[1] += v0.y, o[2] += v0.z, o[3] += v0.w;

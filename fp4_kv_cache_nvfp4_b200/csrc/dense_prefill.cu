@@ -58,8 +58,17 @@ static_assert(DP_OFF_BAR % 8 == 0 && DP_SMEM <= 227 * 1024, "dense prefill layou
 constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 constexpr uint32_t kIdescPV = kIdescS | (1u << 16);  // B (V) has its dims contiguous
 
+// The tensor core's fp32 sums drop bits at every product, towards zero, so the bias
+// of an fp32 result's O grows with its tiles: relative error 2.7e-5 after 128 of
+// them.  After so many tiles of a row tile, O is added, with rounding, to sums in the
+// workspace (they stay in L2), and the products begin anew.  9 x 256 tokens over
+// 16,384 entries: 0.7e-6 and 554 us; after four tiles 1.2e-6 and 466 us, after one
+// 0.45e-6 and 729 us.
+constexpr uint32_t DP_DRAIN = 2;
+
 struct PrefillDenseArgs {
     DenseArgs a;
+    float4* sums;   // [ctas][2 row tiles][32 groups of 4 dims][128 rows] (fp32 results)
     float* part_o;  // [2 * ctas][256 rows][128], times 2^(kPBias - m)
     float* part_m;  // [2 * ctas][256]
     float* part_l;  // [2 * ctas][256]
@@ -370,6 +379,8 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             }
             __syncwarp();
         };
+        // the k-th tile of a row tile (or group) begins O
+        auto fresh = [](uint32_t k) { return SPLIT ? k % DP_DRAIN == 0 : k == 0; };
         auto commit = [&](uint64_t* bar) {
             if (leader) umma_commit(bar);
             __syncwarp();
@@ -400,7 +411,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     if (i) pph1 ^= 1u;
                     else pph0 ^= 1u;
                     tc_fence_after();
-                    mma_pv(i, t - first < 2);
+                    mma_pv(i, fresh((t - first) >> 1));
                     commit(&vempty[vs]);
                     vs ^= 1u;
                     vph ^= vs == 0;
@@ -430,7 +441,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 wait(&pfull[0], pph0);
                 pph0 ^= 1u;
                 tc_fence_after();
-                mma_pv(0, t == first);
+                mma_pv(0, fresh(t - first));
                 if (more) {
                     wait(&kfull[ks], kph);
                     tc_fence_after();
@@ -442,7 +453,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     wait(&pfull[1], pph1);
                     pph1 ^= 1u;
                     tc_fence_after();
-                    mma_pv(1, t == first);
+                    mma_pv(1, fresh(t - first));
                 }
                 commit(&vempty[vs]);
                 vs ^= 1u;
@@ -616,6 +627,9 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                     if (lane == 0 && mine) mbar_arrive(&qfull[i]);
                 }
                 float m = -INFINITY, bias = kPBias, l = 0.f;
+                float m_sum = -INFINITY;
+                bool drained = false;
+                float4* const sums = d.sums + ((size_t)(2 * blockIdx.x + i) * 32) * 128 + r;
                 const uint32_t step = split ? 2u : 1u, n_end = n + (end - t);
                 if (split) {
                     t += (uint32_t)i;
@@ -624,6 +638,29 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 for (; t < end; t += step, n += step, ++sn) {
                     wait(&sfull[i], sn & 1u);
                     tc_fence_after();
+                    if (SPLIT && t - first >= step && ((t - first) / step) % DP_DRAIN == 0) {  // (O is complete: see below)
+                        const float f = m_sum == -INFINITY ? 0.f : ex2(m_sum - m);
+#pragma unroll 1
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t v[32];
+                            tmem_ld32(tO + 32u * x, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float4 u = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                                       __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+                                float4* at = sums + (8 * x + e) * 128;
+                                if (drained) {
+                                    const float4 z = *at;
+                                    u = make_float4(fmaf(z.x, f, u.x), fmaf(z.y, f, u.y), fmaf(z.z, f, u.z), fmaf(z.w, f, u.w));
+                                }
+                                *at = u;
+                            }
+                        }
+                        drained = true;
+                        m_sum = m;
+                        __syncwarp();
+                    }
                     const int nv = seen - (int)(t - w.t0) * DP_KEYS;  // entries of the tile this row sees
                     const uint4 ok = *reinterpret_cast<const uint4*>(smem + DP_OFF_OK + (n & 3u) * 16);
                     const bool all = __all_sync(0xffffffffu, nv >= DP_KEYS && (ok.x & ok.y & ok.z & ok.w) == ~0u);
@@ -732,6 +769,22 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
                 uint8_t* const stage = smem + DP_OFF_Q + (split ? (size_t)(wid & 3) * 16384 : (size_t)i * DP_TILE + (size_t)(wid & 3) * 8192);
                 auto piece_at = [&](int hf, int p) { return reinterpret_cast<uint4*>(stage + (split ? hf * 8192 : 0) + lane * 256 + ((p ^ (lane & 15)) << 4)); };
                 float f0 = 1.f, f1 = 0.f;  // factors of this group's O and the other's
+                // 32 dims of O from 32 x on, with the sums where O moved there before
+                const float f_sum = m_sum == -INFINITY ? 0.f : ex2(m_sum - m);
+                auto load_o = [&](int x, uint32_t (&v)[32]) {
+                    tmem_ld32(tO + 32u * x, v);
+                    tmem_wait_ld();
+                    if (SPLIT && drained) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 z = sums[(8 * x + e) * 128];
+                            v[4 * e] = __float_as_uint(fmaf(z.x, f_sum, __uint_as_float(v[4 * e])));
+                            v[4 * e + 1] = __float_as_uint(fmaf(z.y, f_sum, __uint_as_float(v[4 * e + 1])));
+                            v[4 * e + 2] = __float_as_uint(fmaf(z.z, f_sum, __uint_as_float(v[4 * e + 2])));
+                            v[4 * e + 3] = __float_as_uint(fmaf(z.w, f_sum, __uint_as_float(v[4 * e + 3])));
+                        }
+                    }
+                };
                 if (split) {
                     float2* ml = reinterpret_cast<float2*>(smem + DP_OFF_ML) + r;
                     if (i == 1) {
@@ -739,8 +792,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
 #pragma unroll 1
                         for (int x = 0; x < 4; ++x) {
                             uint32_t v[32];
-                            tmem_ld32(tO + 32u * x, v);
-                            tmem_wait_ld();
+                            load_o(x, v);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 *piece_at(x >> 1, 8 * (x & 1) + e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
@@ -772,8 +824,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
 #pragma unroll 1
                 for (int x = 0; x < 4; ++x) {
                     uint32_t v[32];
-                    tmem_ld32(tO + 32u * x, v);
-                    tmem_wait_ld();
+                    load_o(x, v);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
                     if (split) {
@@ -908,7 +959,8 @@ __global__ void __launch_bounds__(DPJ_THREADS) dense_prefill_join_kernel(const P
 }
 
 size_t dense_prefill_ws_bytes() {
-    return (size_t)2 * kDenseCtas * DP_ROWS * (kD + 2) * 4 + (size_t)2 * kDenseCtas * sizeof(int4);
+    return (size_t)2 * kDenseCtas * DP_ROWS * (kD + 2) * 4 + (size_t)2 * kDenseCtas * sizeof(int4) +
+           (size_t)kDenseCtas * DP_ROWS * kD * 4;
 }
 
 cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stream) {
@@ -934,6 +986,7 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     d.part_m = d.part_o + (size_t)2 * kDenseCtas * DP_ROWS * kD;
     d.part_l = d.part_m + (size_t)2 * kDenseCtas * DP_ROWS;
     d.cut = reinterpret_cast<int4*>(d.part_l + (size_t)2 * kDenseCtas * DP_ROWS);
+    d.sums = reinterpret_cast<float4*>(d.cut + 2 * kDenseCtas);
     // places there can be: units times the longest sequence's tiles and one
     const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS + 1);
     const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);

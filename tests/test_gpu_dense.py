@@ -265,6 +265,22 @@ def test_prefill_a_rising_maximum(csa2):
         check(out, lse, reference(q, c.rows(0), seen_of(L, n, L - n, 1)), str(dt))
 
 
+@pytest.mark.parametrize("B,n,L", [(1, 5, 40000), (2, 40, 12000)])
+def test_fp32_results_do_not_drift(csa2, B, n, L):
+    """A long sequence's fp32 result is as exact as a short one's: within 1e-6 of the
+    definition in the 2-norm (fp32 sums of n terms with rounding; sums that drop bits
+    towards zero, as the tensor core's do, would be n 2^-25 off and reach 1e-5 here)."""
+    c = DenseCase(csa2, [L] * B, 64, seed=L)
+    q = queries(B * n, seed=7)
+    pre = prefill(csa2, c, q, [n * b for b in range(B + 1)], torch.float32)
+    dec = decode(csa2, c, q[::n].contiguous(), torch.float32)
+    for b in range(B):
+        pick = [n * b, n * b + n - 1]
+        ref = reference(q[pick], c.rows(b), [L, L])[0]
+        for got, want in ((pre[0][pick].double().cpu(), ref), (dec[0][b:b + 1].double().cpu(), ref[:1])):
+            assert (got - want).norm() <= 1e-6 * want.norm()
+
+
 def test_prefill_repeatable_and_equal_alone(csa2):
     """The same call twice gives the same bits, and a sequence's result does not
     depend on rows that are not its own beyond its bound."""
