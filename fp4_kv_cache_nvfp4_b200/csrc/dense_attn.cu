@@ -27,7 +27,7 @@ csa2_status dense_args(const csa2_layer_desc* desc, const csa2_kv_cache* cache, 
         return CSA2_ERR_INVALID_ARG;
     if (max_len > (int64_t)cache->max_pages_per_seq * cache->page_size) return CSA2_ERR_INVALID_ARG;
     if (B > kMaxDenseSeqs || rows > kMaxDenseRows || max_len > INT32_MAX - 65536 ||
-        cache->n_phys_pages * cache->page_size > INT32_MAX || B * ((max_len + 63) / 64) > INT32_MAX)
+        cache->n_phys_pages * cache->page_size > INT32_MAX || B * ((max_len + 63) / 64 + 16) > INT32_MAX)
         return CSA2_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256) || ws_bytes < csa2_dense_attn_workspace_bytes(desc, B, prefill))
         return CSA2_ERR_WORKSPACE;
@@ -83,7 +83,7 @@ csa2_status csa2_dense_attn_prefill(const csa2_layer_desc* desc, const csa2_kv_c
     if (s != CSA2_OK || B == 0 || T == 0) return s;
     a.cu_q = cu_q;
     a.q_start = q_start;
-    if (((int64_t)T / 16 + B) * ((max_len + 127) / 128 + 1) > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+    if (((int64_t)T / 16 + B) * ((max_len + 127) / 128 + 8) > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
     return from_cuda(launch_dense_prefill(a, static_cast<char*>(workspace), (cudaStream_t)stream));
 }
 

@@ -35,7 +35,14 @@ constexpr int DD_THREADS = DD_WARPS * 32;
 constexpr int DD_CHUNK = 64;                     // entries per chunk
 constexpr int DD_UNIT = 32;                      // entries per pass over the registers
 constexpr int DD_J = DD_UNIT / 8;                // groups of eight in it
-constexpr uint32_t DD_MIN_SHARE = 4;             // chunks per CTA at least
+constexpr uint32_t DD_MIN_SHARE = 4;             // places per CTA at least
+// A sequence takes a place in the list for each chunk and so many for what it costs
+// besides (its Q and the joining of the warps: about 4 us, in which a CTA scores a
+// dozen chunks).  A multiple of the warps, so that the next sequence's chunks fall to
+// the warps in turn.  64 ragged
+// sequences: 46 us without, 38 with 8 places, 34 with 16; 300 short ones 59, 38, 35.
+constexpr uint32_t DD_WEIGHT = 16;
+static_assert(DD_WEIGHT % DD_WARPS == 0, "whole turns");
 constexpr int DD_STAGES = 2;                     // chunks of a warp's ring
 constexpr int DD_CODES = DD_CHUNK * kCodeBytes;  // 8 KiB per stage
 constexpr int DD_SCALES = DD_CHUNK * kScales;    // 1 KiB
@@ -61,7 +68,7 @@ struct DecodeArgs {
     float* part_o;  // [2 * ctas][16][128], times 2^(kPBias - m)
     float* part_m;  // [2 * ctas][16] maxima (log2 domain)
     float* part_l;  // [2 * ctas][16] sums
-    int4* cut;      // [ctas]: (sequence, its first chunk, its end, first chunk of this CTA) if it begins inside one
+    int4* cut;      // [ctas]: (sequence, its first place, the end of its chunks, first place of this CTA) if it begins inside one
 };
 
 // ---- which chunks ---------------------------------------------------------------
@@ -72,6 +79,7 @@ __device__ __forceinline__ int dense_len(const DenseArgs& a, int b) {
 }
 
 __device__ __forceinline__ uint32_t dd_chunks(int n) { return (uint32_t)(n + DD_CHUNK - 1) / DD_CHUNK; }
+__device__ __forceinline__ uint32_t dd_places(int n) { return n > 0 ? dd_chunks(n) + DD_WEIGHT : 0u; }
 // Offset of 16-byte piece c (0..7) of an entry's row in the swizzled codes
 __device__ __forceinline__ uint32_t dd_piece(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
 
@@ -95,12 +103,12 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
-    // ---- this CTA's share of the chunks: [lo, hi) of the flattened list ------------
+    // ---- this CTA's share: places [lo, hi) of the list -----------------------------
     const int per_thread = (a.B + DD_THREADS - 1) / DD_THREADS;
     const int b0 = min(a.B, tid * per_thread), b1 = min(a.B, b0 + per_thread);
     uint32_t mine = 0;
     for (int b = b0; b < b1; ++b) {
-        mine += dd_chunks(dense_len(a, b));
+        mine += dd_places(dense_len(a, b));
         if (blockIdx.x == 0) {
             const int n = __ldg(a.seq_lens + b);
             if (n < 0 || n > a.max_len) dev_error(a.err, CSA2_DEV_LEN);
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
     if (lo >= before && lo < before + mine) {
         uint32_t t = before;
         for (int b = b0; b < b1; ++b) {
-            const uint32_t n = dd_chunks(dense_len(a, b));
+            const uint32_t n = dd_places(dense_len(a, b));
             if (lo < t + n) {
                 misc[0] = (uint32_t)b;
                 misc[1] = t;
@@ -130,18 +138,29 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
         const int sh = a.page_shift, box_shift = min(sh, kDenseBoxShift), box = 1 << box_shift, n_box = DD_CHUNK >> box_shift;
         uint8_t* const my_codes = smem + DD_OFF_CODES + (size_t)warp * DD_STAGES * DD_CODES;
         uint8_t* const my_scales = smem + DD_OFF_SCALES + (size_t)warp * DD_STAGES * DD_SCALES;
-        int b = (int)misc[0], n = dense_len(a, b);  // the sequence in work, its chunks [t0, t1)
-        uint32_t t0 = misc[1], t1 = t0 + dd_chunks(n);
+        int b = (int)misc[0], n = dense_len(a, b);  // the sequence in work: its chunks [t0, te), its places up to t1
+        uint32_t t0 = misc[1], te = t0 + dd_chunks(n), t1 = te + DD_WEIGHT;
         int pb = b, pn = n, pos_next = -1;          // the same for the next copy; its box's position (-1: none) ...
-        uint32_t p0 = t0, p1 = t1, c_next = lo + (uint32_t)warp;
+        uint32_t p0 = t0, pe = te, c_next = lo + (uint32_t)warp, issued = 0;
         int32_t pg_next = -1;                       // ... and page (not checked yet)
+        auto next_seq = [&](int& x) {  // the next sequence that has entries (there is one), its length
+            int len;
+            do len = dense_len(a, ++x);
+            while (len == 0 && x + 1 < a.B);
+            return len;
+        };
+        auto skip = [](uint32_t& c, uint32_t s1) {  // the warp's first place from s1 on
+            if (c < s1) c += (s1 - c + DD_WARPS - 1) / DD_WARPS * DD_WARPS;
+        };
         auto seek = [&]() {
-            if (c_next >= hi) return;
-            while (c_next >= p1) {  // the next sequence that has chunks
-                pn = dense_len(a, ++pb);
-                p0 = p1;
-                p1 += dd_chunks(pn);
+            while (c_next < hi && c_next >= pe) {  // the next sequence that has chunks
+                skip(c_next, pe + DD_WEIGHT);
+                if (c_next >= hi) return;
+                p0 = pe + DD_WEIGHT;
+                pn = next_seq(pb);
+                pe = p0 + dd_chunks(pn);
             }
+            if (c_next >= hi) return;
             pos_next = (int)(c_next - p0) * DD_CHUNK + lane * box;
             if (lane >= n_box || pos_next >= pn) pos_next = -1;
             else pg_next = __ldg(a.cache.page_table + (int64_t)pb * a.cache.max_pages_per_seq + (pos_next >> sh));
@@ -160,6 +179,7 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                 bulk_load(my_scales + (size_t)st * DD_SCALES + (size_t)lane * box * kScales,
                           a.cache.scales + (int64_t)slot * kScales, (uint32_t)box * kScales, &full[st]);
             }
+            ++issued;
             c_next += DD_WARPS;
             seek();
             return boxes;
@@ -182,15 +202,19 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
         float* slab = reinterpret_cast<float*>(smem + DD_OFF_SLAB);
         float* wm = reinterpret_cast<float*>(smem + DD_OFF_M);
         float* wl = reinterpret_cast<float*>(smem + DD_OFF_L);
-        if (tid == 0) d.cut[blockIdx.x] = lo > t0 ? make_int4(b, (int)t0, (int)t1, (int)lo) : make_int4(-1, 0, 0, 0);
+        if (tid == 0) d.cut[blockIdx.x] = lo > t0 && lo < te ? make_int4(b, (int)t0, (int)te, (int)lo) : make_int4(-1, 0, 0, 0);
         uint32_t t = lo, c = lo + (uint32_t)warp, done = 0;  // c: this warp's chunk, its number `done`
         while (t < hi) {
-            while (t >= t1) {
-                n = dense_len(a, ++b);
+            if (t >= te) {  // the next sequence that has chunks
+                t = t1;
+                if (t >= hi) break;
+                skip(c, t1);
+                n = next_seq(b);
                 t0 = t1;
-                t1 += dd_chunks(n);
+                te = t0 + dd_chunks(n);
+                t1 = te + DD_WEIGHT;
             }
-            const uint32_t seg0 = t, seg1 = min(hi, t1);
+            const uint32_t seg0 = t, seg1 = min(hi, te);
             t = seg1;
             // ---- Q of the sequence: heads g and g + 8, channels 32 t .. 32 t + 31 -------
             uint32_t qa[8][4];
@@ -259,7 +283,7 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                 }
                 const int st = (int)(done & 1u);
                 if (!mbar_wait(&full[st], (done >> 1) & 1u, kDenseWaitLimit)) {  // give up: no copy stays in flight
-                    if (c_next - c > DD_WARPS) mbar_wait(&full[st ^ 1], ((done + 1) >> 1) & 1u, kDenseWaitLimit);
+                    if (issued > done + 1) mbar_wait(&full[st ^ 1], ((done + 1) >> 1) & 1u, kDenseWaitLimit);
                     if (lane == 0) dev_error(a.err, CSA2_DEV_TIMEOUT);
                     c = c_next = hi;
                     break;
@@ -460,7 +484,7 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                     o[0] += v0.x, o[1] += v0.y, o[2] += v0.z, o[3] += v0.w;
                     o[4] += v1.x, o[5] += v1.y, o[6] += v1.z, o[7] += v1.w;
                 }
-                if (seg0 == t0 && seg1 == t1) {  // the whole sequence
+                if (seg0 == t0 && seg1 == te) {  // the whole sequence
                     dense_store(a, (int64_t)b * kH + h, d8, o, M, l);
                 } else {
                     const int64_t part = 2 * (int64_t)blockIdx.x + (seg0 == t0 ? 1 : 0);
@@ -576,7 +600,7 @@ cudaError_t launch_dense_decode(const DenseArgs& a, char* ws, cudaStream_t strea
     d.part_m = d.part_o + (size_t)2 * kDenseCtas * kH * kD;
     d.part_l = d.part_m + (size_t)2 * kDenseCtas * kH;
     d.cut = reinterpret_cast<int4*>(d.part_l + (size_t)2 * kDenseCtas * kH);
-    const int64_t most = (int64_t)a.B * ((a.max_len + DD_CHUNK - 1) / DD_CHUNK);  // chunks there can be
+    const int64_t most = (int64_t)a.B * ((a.max_len + DD_CHUNK - 1) / DD_CHUNK + DD_WEIGHT);  // places there can be
     const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);
     LaunchCfg c(dim3(ctas), dim3(DD_THREADS), DD_SMEM, stream);
     e = a.out_bf16 ? cudaLaunchKernelEx(&c.cfg, dense_decode_kernel<false>, (const CUtensorMap)map, d)

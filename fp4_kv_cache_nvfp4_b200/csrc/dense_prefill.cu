@@ -36,6 +36,7 @@
 namespace csa2 {
 
 constexpr int DP_TOK = 16;                       // tokens per unit (8 per row tile)
+constexpr uint32_t DP_WEIGHT = 3;                // places of a unit besides its tiles': ragged prompts 124 us with 1, 103 with 3
 constexpr int DP_ROWS = DP_TOK * kH;             // 256
 constexpr int DP_KEYS = 128;                     // entries per tile
 constexpr uint32_t DP_HALF = 128 * 128;          // 64 channels of an operand tile: [128 rows][128 B], swizzled
@@ -109,8 +110,8 @@ __device__ __forceinline__ uint32_t unit_tiles(const DenseArgs& a, const SeqQ& s
     return max(1u, (uint32_t)(seen_by(a, s, min((k + 1) * DP_TOK, s.nq) - 1) + DP_KEYS - 1) / DP_KEYS);
 }
 // Places in the list of the units before k: a unit takes one for each tile and
-// one for what it costs besides (its Q, its rows: as long as a tile or two, which
-// counts where the units are short).  With A = p0 + 16 + 127 r and D = 128 r, a
+// DP_WEIGHT for what it costs besides (its Q, its rows: as long as a tile or two,
+// which counts where the units are short).  With A = p0 + 16 + 127 r and D = 128 r, a
 // full unit i has min(C, floor((A + 16 i) / D)) tiles, C = ceil(len / 128): a
 // staircase, whose sum is a difference of G(x) = sum_{j < x} floor(j / (8 r)).
 __device__ __forceinline__ uint64_t places_before(const DenseArgs& a, const SeqQ& s, int k) {
@@ -132,14 +133,14 @@ __device__ __forceinline__ uint64_t places_before(const DenseArgs& a, const SeqQ
         };
         n = (uint64_t)(G(x + ic) - G(x)) + (uint64_t)(m - ic) * C;
     }
-    return (k > last ? n + unit_tiles(a, s, last) : n) + (uint64_t)k;
+    return (k > last ? n + unit_tiles(a, s, last) : n) + (uint64_t)k * DP_WEIGHT;
 }
 
 // Walks the units of a CTA's share in order.
 struct Walk {
     int b, k, nk;
     SeqQ s;
-    uint32_t t0, te;  // the unit's tiles in the list; its last place is te
+    uint32_t t0, te;  // the unit's tiles in the list; its other places follow
     __device__ __forceinline__ void start(const DenseArgs& a, const uint32_t* at) {
         b = (int)at[0];
         k = (int)at[1];
@@ -149,7 +150,7 @@ struct Walk {
         te = t0 + unit_tiles(a, s, k);
     }
     __device__ __forceinline__ void next(const DenseArgs& a) {
-        t0 = te + 1;
+        t0 = te + DP_WEIGHT;
         if (++k >= nk) {
             k = 0;
             do {
@@ -162,8 +163,9 @@ struct Walk {
     // The first tile at or behind place t, and the end of the CTA's tiles of its unit.
     // False: there is none before hi.
     __device__ __forceinline__ bool tiles(const DenseArgs& a, uint32_t& t, uint32_t hi, uint32_t& end) {
-        if (t < hi && t == te) {
-            if (++t < hi) next(a);
+        if (t < hi && t >= te) {
+            t = te + DP_WEIGHT;
+            if (t < hi) next(a);
         }
         end = min(hi, te);
         return t < hi;
@@ -987,8 +989,8 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     d.part_l = d.part_m + (size_t)2 * kDenseCtas * DP_ROWS;
     d.cut = reinterpret_cast<int4*>(d.part_l + (size_t)2 * kDenseCtas * DP_ROWS);
     d.sums = reinterpret_cast<float4*>(d.cut + 2 * kDenseCtas);
-    // places there can be: units times the longest sequence's tiles and one
-    const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS + 1);
+    // places there can be: units times the longest sequence's tiles and the weight
+    const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS + DP_WEIGHT);
     const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);
     LaunchCfg c(dim3(ctas), dim3(DP_THREADS), DP_SMEM, stream);
     // By the average tokens of a sequence (cu_q is on the device): at most one row
