@@ -436,7 +436,8 @@ def kv_pages_copy(caches: list[KVCache], src, dst, err=None, stream=None) -> Non
 
 def kv_pages_fork(caches: list[KVCache], refs, seq_lens, parents, children, workspace: torch.Tensor, err=None,
                   stream=None) -> None:
-    """Rows children[i] of the caches' page table share what rows parents[i] hold."""
+    """Rows children[i] of the caches' page table share what rows parents[i] hold.
+    Caches of one call share the table itself (build them on one CUDA tensor)."""
     C, table, dev = _page_args(caches, refs, seq_lens, err)
     _on_gpu("parents", parents, _I32T, (None,), dev)
     _on_gpu("children", children, _I32T, (parents.numel(),), dev)

@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
 #pragma unroll
                 for (int w = 0; w < DD_WARPS; ++w) {
                     const float mw = wm[w * kH + h];
-                    if (mw != -INFINITY) l += wl[w * kH + h] * ex2(mw - M);
+                    l += mw == -INFINITY ? wl[w * kH + h] : wl[w * kH + h] * ex2(mw - M);  // (0, or the NaN of scores that all are)
                 }
 #pragma unroll
                 for (int w = 0; w < DD_WARPS; ++w) {
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(DJ_THREADS) dense_decode_join_kernel(const Dec
     pdl_trigger();
     const int4 cut = d.cut[c];
     if (cut.x < 0) return;
-    const int per = cut.w / c;  // CTA c begins at chunk c * per
+    const int per = cut.w / c;  // CTA c begins at place c * per
     if (cut.y < (c - 1) * per) return;  // an earlier CTA's block does it
     const int last = (cut.z - 1) / per, n = last - c + 2;
     const int h = 4 * blockIdx.y + (warp >> 2), w4 = warp & 3;

@@ -360,7 +360,8 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
  * (length 0, or a causal mask that leaves none) gets out = 0, lse = -inf.
  * What is not seen has no influence, whatever it holds (a NaN scale, a missing
  * page).  Of an entry that is seen, a NaN scale of K makes the results of the
- * tokens that see it NaN, one of V at least the 16 channels it covers.
+ * tokens that see it NaN, one of V at least the 16 channels it covers; a NaN
+ * in a query's head makes that head's results NaN, out and lse, and no others.
  * Detected on the device: a length outside [0, max_len] or a negative
  * q_start (CSA2_DEV_LEN; the sequence counts as empty), a range of cu_q that
  * is not ascending or not inside [0, T] (CSA2_DEV_LEN; that sequence's rows

@@ -393,6 +393,90 @@ def test_dense_and_window_equal_the_sparse_step(csa2):
     assert (out - want).abs().max() <= 2e-3 and (lse - want_lse).abs().max() <= 2e-3  # the sparse path's tolerance
 
 
+def test_many_short_sequences_and_large_pages(csa2):
+    """More sequences than CTAs, some empty; pages larger than a tile."""
+    lens = [(37 * b) % 300 for b in range(400)]
+    c = DenseCase(csa2, lens, 16, seed=40)
+    q = queries(400, seed=41)
+    out, lse, err = decode(csa2, c, q, torch.bfloat16)
+    outp, lsep, errp = prefill(csa2, c, q, list(range(401)), torch.float32, [max(0, n - 1) for n in lens])
+    assert err == errp == 0
+    for b in (0, 1, 73, 147, 148, 299, 300, 399):
+        ref = reference(q[b:b + 1], c.rows(b), [lens[b]])
+        check(out[b:b + 1], lse[b:b + 1], ref, f"decode {b}")
+        check(outp[b:b + 1], lsep[b:b + 1], reference(q[b:b + 1], c.rows(b), [min(lens[b], max(0, lens[b] - 1) + 1)]), f"prefill {b}")
+    c = DenseCase(csa2, [5000, 1025], 1024, seed=42)
+    q = queries(2, seed=43)
+    out, lse, err = decode(csa2, c, q, torch.float32)
+    for b in range(2):
+        check(out[b:b + 1], lse[b:b + 1], reference(q[b:b + 1], c.rows(b), [c.lens[b]]), f"pages of 1024, {b}")
+
+
+def test_nothing_to_see(csa2):
+    """No entries in any sequence; no tokens in any sequence."""
+    c = DenseCase(csa2, [0, 0, 0], 64)
+    q = queries(3)
+    for dt in DT.values():
+        out, lse, err = decode(csa2, c, q, dt)
+        assert err == 0 and (out == 0).all() and (lse == -math.inf).all()
+        out, lse, err = prefill(csa2, c, q, [0, 2, 2, 3], dt)
+        assert err == 0 and (out == 0).all() and (lse == -math.inf).all()
+        out, lse, err = prefill(csa2, c, q, [1, 1, 1, 1], dt, [0, 0, 0])
+        assert err == 0 and (out == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("n", [1, 65, 129])
+def test_a_lone_bad_entry(csa2, n):
+    """The only entries that some part of the work sees have NaN scales of K: the sum of that part counts."""
+    c = DenseCase(csa2, [n], 64, seed=5)
+    c.cache.scales[c.slots(0, n)[-1], :8] = 0x7F
+    q = queries(1)
+    for dt in DT.values():
+        for out, lse in (decode(csa2, c, q, dt)[:2], prefill(csa2, c, q, [0, 1], dt, [n - 1])[:2]):
+            assert torch.isnan(lse).all() and torch.isnan(out).all()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_query_is_its_heads_alone(csa2, bad):
+    c = DenseCase(csa2, [333], 64, seed=3)
+    q = queries(12)
+    q[3, 5, 17] = bad
+    rest = torch.ones((12, 16), dtype=torch.bool)
+    rest[3, 5] = False
+    for dt in DT.values():
+        for out, lse in ((prefill(csa2, c, q, [0, 12], dt, [321])[:2]),
+                         [torch.cat([decode(csa2, c, q[i:i + 1], dt, lens=[322 + i])[k] for i in range(12)]) for k in (0, 1)]):
+            assert torch.isnan(out[3, 5]).all() and torch.isnan(lse[3, 5])
+            clean = queries(12)
+            ref = reference(clean, c.rows(0), seen_of(333, 12, 321, 1))
+            for i in range(12):
+                keep = rest[i].cuda()
+                check(out[i:i + 1, keep], lse[i:i + 1, keep], tuple(x[i:i + 1, rest[i]] for x in ref), f"token {i}")
+
+
+def test_prefills_on_two_streams(csa2):
+    """Calls that run side by side, each with its own workspace, do not disturb one another."""
+    d = csa2.default_desc(csa2.FULL, 1)
+    cs = [DenseCase(csa2, [2000, 700], 64, seed=s) for s in (1, 2)]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu, st, sl = i32([0, 100, 130]), i32([1900, 670]), i32([2000, 700])
+    qs = [queries(130, seed=s).cuda() for s in (3, 4)]
+    want = [prefill(csa2, c, q.cpu(), [0, 100, 130], torch.bfloat16, [1900, 670])[:2] for c, q in zip(cs, qs)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    ws = [torch.empty(csa2.dense_attn_workspace_bytes(d, 2, True), dtype=torch.uint8, device="cuda") for _ in cs]
+    out = [[torch.empty((130, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(4)] for _ in cs]
+    lse = [[torch.empty((130, 16), device="cuda") for _ in range(4)] for _ in cs]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for k in range(2):
+            csa2.dense_attn_prefill(d, cs[k].cache, qs[k], cu, sl, out[k][i], lse[k][i], cs[k].max_len, ws[k],
+                                    q_start=st, stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        for i in range(4):
+            assert torch.equal(out[k][i], want[k][0]) and torch.equal(lse[k][i], want[k][1])
+
+
 def test_main_kv_in_host_memory_is_refused(csa2):
     c = csa2.KVCache(4, 64, torch.arange(4, dtype=torch.int32).view(1, 4), main_kv_on_host=True)
     d = csa2.default_desc(csa2.FULL, 1)

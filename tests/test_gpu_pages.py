@@ -227,6 +227,41 @@ def test_fork_refusals_on_the_device(csa2):
     p.d_fork([0, 2], [3, 4]); p.fork([0, 2], [3, 4]); p.check(DEV_PAGE)  # noqa: E702
 
 
+def test_a_main_kv_in_pinned_host_memory(csa2):
+    """Forks and compactions of a tiered cache: codes and scales in mapped host memory."""
+    table = torch.tensor([[5, 2, -1], [-1, -1, -1]], dtype=torch.int32).cuda()
+    c = csa2.KVCache(6, 8, table, main_kv_on_host=True)
+    g = torch.Generator().manual_seed(1)
+    for t in (c.codes, c.scales):
+        t.copy_(torch.randint(0, 256, t.shape, generator=g, dtype=torch.uint8))
+    want = [t.clone() for t in (c.codes, c.scales)]
+    refs = torch.tensor([0, 0, 1, 0, 0, 1], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([13, 0], dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.empty(csa2.kv_pages_workspace_bytes(6, 1), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    csa2.kv_pages_fork([c], refs, lens, i32([0]), i32([1]), ws, err=err)
+    m, n = i32([0] * 6), i32([0])
+    csa2.kv_pages_compact([c], refs, m, n, ws, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0 and int(n) == 3 and m.tolist() == [0, -1, 2, -1, -1, 1]
+    assert c.page_table.tolist() == [[1, 2, -1], [1, 0, -1]] and refs.tolist() == [1, 2, 1, 0, 0, 0]
+    for t, w in zip((c.codes, c.scales), want):
+        v, w = t.view(6, -1), w.view(6, -1)
+        assert torch.equal(v[0], w[2]) and torch.equal(v[1], w[5]) and torch.equal(v[2], w[2])
+
+
+def test_caches_that_kernels_cannot_write_are_refused(csa2):
+    z = lambda *s, dt=torch.uint8: torch.zeros(s, dtype=dt)  # noqa: E731
+    c = csa2.KVCache.from_tensors(z(64, 128), z(64, 16), z(2, 4, dt=torch.int32).cuda(), 8)
+    refs, lens = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (8, 2))
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(csa2.kv_pages_workspace_bytes(8, 1), dtype=torch.uint8, device="cuda")
+    for bad in (lambda: csa2.kv_pages_copy([c], one, one), lambda: csa2.kv_pages_fork([c], refs, lens, one, one, ws)):
+        with pytest.raises(ValueError):
+            bad()
+
+
 def test_fork_until_the_pool_is_empty(csa2):
     p = Pool(csa2, [20, 16, 33], 10, 12, 8)       # 3 + 2 + 5 pages, two free
     par, chi = [0, 1, 2, 0, 1], [3, 4, 5, 6, 7]
