@@ -365,7 +365,9 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
  * Detected on the device: a length outside [0, max_len] or a negative
  * q_start (CSA2_DEV_LEN; the sequence counts as empty), a range of cu_q that
  * is not ascending or not inside [0, T] (CSA2_DEV_LEN; that sequence's rows
- * stay as they were), a missing page (CSA2_DEV_PAGE; its entries count as not
+ * stay as they were; if the other ranges then overlap, a row gets one of its
+ * sequences' results, or, where they would be more work than T rows can be,
+ * none does), a missing page (CSA2_DEV_PAGE; its entries count as not
  * seen).  Results do not vary from run to run.
  * q and out must be 16-byte aligned, codes and scales in device memory
  * (UNSUPPORTED if they are in host memory: these calls read them whole), the
@@ -393,7 +395,8 @@ CSA2_API csa2_status csa2_dense_attn_prefill(const csa2_layer_desc* desc, const 
  *               whose pages share one numbering and one table: a model's
  *               Full layers.  page_size, max_pages_per_seq and n_phys_pages
  *               (<= 2^22) must be equal; codes and scales, and idx_k and
- *               idx_k_pooled where they are not NULL, are copied
+ *               idx_k_pooled where they are not NULL, are copied (idx_k_pooled
+ *               only beside idx_k)
  *   page_table  [n_seqs][max_pages_per_seq] int32, -1 where there is no page
  *               (rewritten by these calls; the caches' own page_table is not read)
  *   refs        [n_phys_pages] int32, 16-byte aligned: how many entries of the

@@ -412,6 +412,26 @@ def test_many_short_sequences_and_large_pages(csa2):
         check(out[b:b + 1], lse[b:b + 1], reference(q[b:b + 1], c.rows(b), [c.lens[b]]), f"pages of 1024, {b}")
 
 
+def test_ranges_that_overlap_without_end(csa2):
+    """Ranges that go back to row 0 again and again: their places in the list of
+    work pass 32 bits, though T and the lengths are in bounds.  Nothing is done."""
+    B, T, page, cols = 1024, 4096, 1 << 16, 64
+    table = torch.full((B, cols), -1, dtype=torch.int32, device="cuda")
+    cache = csa2.KVCache.from_tensors(torch.zeros((page, 128), dtype=torch.uint8, device="cuda"),
+                                      torch.zeros((page, 16), dtype=torch.uint8, device="cuda"), table, page)
+    d = csa2.default_desc(csa2.FULL, 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu, sl = i32([0, T] * (B // 2) + [0]), i32([page * cols] * B)
+    out = torch.full((T, 16, 128), 7.0, device="cuda")
+    lse = torch.full((T, 16), 7.0, device="cuda")
+    ws = torch.empty(csa2.dense_attn_workspace_bytes(d, B, True), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert (B // 2) * (T // 16) * (page * cols // 128 + 1) > 2**32
+    csa2.dense_attn_prefill(d, cache, queries(T).cuda(), cu, sl, out, lse, page * cols, ws, err=err)
+    torch.cuda.synchronize()
+    assert int(err) & DEV_LEN and (out == 7).all() and (lse == 7).all()
+
+
 def test_nothing_to_see(csa2):
     """No entries in any sequence; no tokens in any sequence."""
     c = DenseCase(csa2, [0, 0, 0], 64)
