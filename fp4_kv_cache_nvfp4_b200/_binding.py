@@ -394,12 +394,12 @@ def kv_pages_workspace_bytes(n_phys_pages: int, n: int = 0) -> int:
     return size
 
 
-def _mapped(caches) -> None:
-    """Every array of the caches is where kernels can write it."""
+def _mapped(caches, dev: int) -> None:
+    """Every array of the caches is where kernels of GPU `dev` can write it."""
     for c in caches:
         for t in (c.codes, c.scales, c.idx_k, c.pooled):
-            if t is not None and not t.is_cuda and not t.is_pinned():
-                raise ValueError(f"a cache's array is on {t.device} and not pinned")
+            if t is not None and t.get_device() != dev and (t.is_cuda or not t.is_pinned()):
+                raise ValueError(f"a cache's array is on {t.device}: neither on cuda:{dev} nor pinned")
 
 
 def _page_args(caches, refs, seq_lens, err):
@@ -409,7 +409,7 @@ def _page_args(caches, refs, seq_lens, err):
     c0 = caches[0]
     table = c0.page_table
     dev = _device(table)
-    _mapped(caches)
+    _mapped(caches, dev)
     for c in caches[1:]:
         if c.page_table.data_ptr() != table.data_ptr() or c.page_table.shape != table.shape:
             raise ValueError("caches: they do not share one page table")
@@ -425,7 +425,7 @@ def kv_pages_copy(caches: list[KVCache], src, dst, err=None, stream=None) -> Non
     if not caches:
         raise ValueError("caches: empty")
     dev = _device(src)
-    _mapped(caches)
+    _mapped(caches, dev)
     _on_gpu("src", src, _I32T, (None,), dev)
     _on_gpu("dst", dst, _I32T, (src.numel(),), dev)
     _on_gpu("err", err, _I32T, (1,), dev, optional=True)

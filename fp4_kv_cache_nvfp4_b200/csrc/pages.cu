@@ -452,7 +452,7 @@ csa2_status page_caches(int32_t n, const csa2_kv_cache* caches, PageCaches& p) {
         const csa2_kv_cache& c = caches[i];
         const csa2_status s = check_cache(&c, false, false);
         if (s != CSA2_OK) return s;
-        if (c.idx_k && !aligned(c.idx_k, 16)) return CSA2_ERR_INVALID_ARG;
+        if (c.idx_k ? !aligned(c.idx_k, 16) : c.idx_k_pooled != nullptr) return CSA2_ERR_INVALID_ARG;
         if (c.page_size != p.page_size || c.n_phys_pages != caches[0].n_phys_pages ||
             c.max_pages_per_seq != caches[0].max_pages_per_seq)
             return CSA2_ERR_INVALID_ARG;

@@ -85,3 +85,11 @@ def test_binding_checks_tensors(csa2):
                 lambda: csa2.kv_pages_copy([a], z(1), z(1))):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_pooled_alone_is_refused(csa2):
+    """Pooled indexer keys without the keys they pool: they would not be copied."""
+    for what in ("copy", "fork", "compact"):
+        assert _call(csa2, what, _caches(csa2, 2, idx_k=None)) == 1
+        assert _call(csa2, what, _caches(csa2, 2, idx_k=None, idx_k_pooled=None), n=0, table=None) == \
+            (0 if what != "compact" else 1)
