@@ -24,6 +24,9 @@
 // tensor core, the 16,384 exponentials 1024 cycles of the special-function
 // units, and the products' operands with the dequantised tiles' writes about 1000
 // cycles of shared memory, so three units are near their limits at once.
+// Measured: the last 4096 of 32,768 tokens at ratio 2 (16,384 entries) 485 to 497 us,
+// 1040 to 1060 TFLOP/s of the products that the mask leaves; drafts of 8 x 5 tokens
+// over 65,536 entries 72 us.
 #include <string.h>
 
 #include <algorithm>
@@ -63,7 +66,7 @@ constexpr uint32_t kIdescPV = kIdescS | (1u << 16);  // B (V) has its dims conti
 // of an fp32 result's O grows with its tiles: relative error 2.7e-5 after 128 of
 // them.  After so many tiles of a row tile, O is added, with rounding, to sums in the
 // workspace (they stay in L2), and the products begin anew.  9 x 256 tokens over
-// 16,384 entries: 0.7e-6 and 554 us; after four tiles 1.2e-6 and 466 us, after one
+// 16,384 entries: 0.7e-6 and 567 us; after four tiles 1.2e-6 and 477 us, after one
 // 0.45e-6 and 729 us.
 constexpr uint32_t DP_DRAIN = 2;
 
@@ -1011,8 +1014,8 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     LaunchCfg c(dim3(ctas), dim3(DP_THREADS), DP_SMEM, stream);
     // By the average tokens of a sequence (cu_q is on the device): at most one row
     // tile's take the paired kernel.  Measured, paired / not: 8 x 5 tokens over 65,536
-    // entries 77.0 / 83.4 us, 8 x 5 over 32,768 50.2 / 52.1; 4096 tokens over 16,384
-    // entries 497 / 485 us.
+    // entries 72 / 81 us, 8 x 5 over 32,768 46 / 49, 200 x 5 over 400 to 4,000 60 / 63;
+    // 4096 tokens over 16,384 entries 497 / 485 us.
     const bool paired = a.T <= DP_TOK / 2 * (int64_t)a.B;
     auto kernel = a.out_bf16 ? (paired ? dense_prefill_kernel<false, true> : dense_prefill_kernel<false, false>)
                              : (paired ? dense_prefill_kernel<true, true> : dense_prefill_kernel<true, false>);

@@ -10,6 +10,9 @@
 // page-table entry, and page_size * 288 bytes read and written for a page that
 // is copied (codes 128, scales 16, indexer K 128 and pooled indexer K 16 bytes
 // per entry).
+// Small requests are bound by their two or three launches (about 10 us in a graph,
+// each waiting for the one before it), large ones by HBM.  Measured: 256 forks in 3
+// caches 19 us, compacting 12,000 pages 30 us (3.3 TB/s).
 #include <algorithm>
 
 #include "checks.h"
