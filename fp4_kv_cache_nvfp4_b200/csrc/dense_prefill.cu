@@ -324,9 +324,20 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
     const uint32_t mine = (uint32_t)sum;
     uint32_t total;
     const uint32_t before = block_excl_scan(mine, reinterpret_cast<uint32_t*>(smem + DP_OFF_SCAN), &total);
+    // The host's bound on the places holds while no ranges overlap, which only a range
+    // that is not ascending makes possible.  Then the places are counted again, in units
+    // of 2^16 (rounded down: below 2^15 of them the sum above has not wrapped), and a
+    // call whose places do not fit does nothing.
+    if (__syncthreads_or(!ascending)) {
+        uint32_t coarse;
+        block_excl_scan((uint32_t)min(sum >> 16, (uint64_t)1 << 16), reinterpret_cast<uint32_t*>(smem + DP_OFF_SCAN), &coarse);
+        if (coarse >= 1u << 15 || total > (uint32_t)INT32_MAX) {
+            total = 0;
+            if (tid == 0) dev_error(a.err, CSA2_DEV_LEN);
+        }
+    }
     const uint32_t per = (total + gridDim.x - 1) / gridDim.x;
-    const uint32_t lo = min(total, per * blockIdx.x);
-    uint32_t hi = min(total, lo + per);
+    const uint32_t lo = min(total, per * blockIdx.x), hi = min(total, lo + per);
     if (lo < hi && lo >= before && lo < before + mine) {
         uint32_t t = before;
         for (int b = b0; b < b1; ++b) {
@@ -347,19 +358,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             t += n;
         }
     }
-    // The host's bound on the places holds while no ranges overlap, which only a range
-    // that is not ascending makes possible.  Then the places are counted again, in units
-    // of 2^16 (rounded down: below 2^15 of them the sum above has not wrapped), and a
-    // call whose places do not fit does nothing.
-    if (__syncthreads_or(!ascending)) {
-        uint32_t coarse;
-        block_excl_scan((uint32_t)min(sum >> 16, (uint64_t)1 << 16), reinterpret_cast<uint32_t*>(smem + DP_OFF_SCAN), &coarse);
-        if (coarse >= 1u << 15 || total > (uint32_t)INT32_MAX) {
-            hi = lo;
-            if (tid == 0) dev_error(a.err, CSA2_DEV_LEN);
-        }
-        __syncthreads();
-    }
+    __syncthreads();
     // bounded; a thread that gave up once does not wait any more
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
