@@ -14,9 +14,9 @@
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, one thread per row: maximum,
 //                   P = 2^(S c - m) as fp16 back into TMEM over S, the sum;
 //                   O's rescaling when m rises (rare); the result's rows
-//   warps 8-11      K and V of the next tiles: FP4 read with plain loads one tile
+//   4 or 6 more     K and V of the next tiles: FP4 read with plain loads one tile
 //                   ahead, dequantised to fp16 (exact) into swizzled shared tiles
-//   warp 12         issues the products: while one row tile is in its softmax, the
+//   the last one    issues the products: while one row tile is in its softmax, the
 //                   other's products run
 // TMEM: S of both row tiles (P over them), O of both: all 512 columns.
 //
@@ -26,7 +26,7 @@
 // cycles of shared memory, so three units are near their limits at once.
 // Measured: the last 4096 of 32,768 tokens at ratio 2 (16,384 entries) 485 to 497 us,
 // 1040 to 1060 TFLOP/s of the products that the mask leaves; drafts of 8 x 5 tokens
-// over 65,536 entries 72 us.
+// over 65,536 entries 69 us.
 #include <string.h>
 
 #include <algorithm>
@@ -44,10 +44,14 @@ constexpr int DP_ROWS = DP_TOK * kH;             // 256
 constexpr int DP_KEYS = 128;                     // entries per tile
 constexpr uint32_t DP_HALF = 128 * 128;          // 64 channels of an operand tile: [128 rows][128 B], swizzled
 constexpr uint32_t DP_TILE = 2 * DP_HALF;        // 32 KiB
-constexpr int DP_W_CONV = 8, DP_NCONV = 4, DP_W_MMA = 12, DP_WARPS = 13;  // four warps a scheduler at most: 128 registers a thread
-constexpr int DP_THREADS = DP_WARPS * 32;
-constexpr int DP_STEP = DP_NCONV * 8;            // a converter thread's entries are that far apart ...
-constexpr int DP_ENT = DP_KEYS / DP_STEP;        // ... and so many
+constexpr int DP_W_CONV = 8;                     // the first converter warp; the one that issues follows the last
+// Converter warps.  Sixteen warps leave a thread 128 registers, as thirteen do.  The
+// paired kernel takes an entry tile for one row tile, not for two, and waits for the
+// conversion: with four 73.5 us (8 x 5 tokens over 65,536 entries), with six 69.4, with
+// seven 69.4; without pairs four 486 us (4096 over 16,384 entries), six 516: they
+// issue beside the softmax.  With three (168 registers, no spills) 82 and 513.
+constexpr int dp_conv(bool paired) { return paired ? 6 : 4; }
+constexpr int dp_threads(bool paired) { return (DP_W_CONV + dp_conv(paired) + 1) * 32; }
 constexpr size_t DP_OFF_Q = 0;                            // [2 row tiles]
 constexpr size_t DP_OFF_K = DP_OFF_Q + 2 * DP_TILE;       // [2 slots]
 constexpr size_t DP_OFF_V = DP_OFF_K + 2 * DP_TILE;       // [2 slots]
@@ -268,7 +272,9 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // SPLIT: P as two fp16 terms (fp32 results).  PAIRED: units of one row tile use
 // both groups of softmax warps.
 template <bool SPLIT, bool PAIRED>
-__global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const PrefillDenseArgs d) {
+__global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(const PrefillDenseArgs d) {
+    constexpr int NCONV = dp_conv(PAIRED), W_MMA = DP_W_CONV + NCONV;
+    constexpr int STEP = NCONV * 8, ENT = (DP_KEYS + STEP - 1) / STEP;  // a converter thread has at most ENT entries, STEP apart
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const DenseArgs& a = d.a;
@@ -286,9 +292,9 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&kfull[i], DP_NCONV);
+            mbar_init(&kfull[i], NCONV);
             mbar_init(&kempty[i], 1);
-            mbar_init(&vfull[i], DP_NCONV);
+            mbar_init(&vfull[i], NCONV);
             mbar_init(&vempty[i], 1);
             mbar_init(&qfull[i], 4);
             mbar_init(&sfull[i], 1);
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         *s_timeout = 0;
         fence_mbar_init();
     }
-    if (wid == DP_W_MMA) {
+    if (wid == W_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(misc)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
     pdl_trigger();
 
     // ---- this CTA's share: places [lo, hi) of the list -----------------------------
-    const int per_thread = (a.B + DP_THREADS - 1) / DP_THREADS;
+    const int per_thread = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;
     const int b0 = min(a.B, tid * per_thread), b1 = min(a.B, b0 + per_thread);
     uint64_t sum = 0;
     bool ascending = true;
@@ -368,7 +374,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         }
     };
 
-    if (lo < hi && wid == DP_W_MMA) {
+    if (lo < hi && wid == W_MMA) {
         // ================= the products: every lane keeps the books, one issues =================
         const bool leader = elect_one();
         Walk w;
@@ -490,12 +496,13 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
         if (!mbar_wait(mma_done, 0u, kDenseWaitLimit)) *s_timeout = 1;
     } else if (lo < hi && wid >= DP_W_CONV) {
         // ================= converters: FP4 rows -> fp16 operand tiles =================
-        // Thread ct owns quarter qt (32 channels of K and of V) of entries e0 + DP_STEP i.
+        // Thread ct owns quarter qt (32 channels of K and of V) of entries e0 + STEP i.
         const int ct = tid - DP_W_CONV * 32, qt = ct & 3, e0 = ct >> 2, cw = wid - DP_W_CONV;
         // The two quarters of a 64-channel half write their four 16-byte pieces one
         // after the other, the other half's begin with the third, so that eight lanes
         // write to distinct banks; the codes are loaded in that order.
         const int rot = qt >> 1;
+        auto mine = [&](int i) { return STEP * (i + 1) <= DP_KEYS || STEP * i + 8 * cw < DP_KEYS; };  // (the same in a warp)
         uint32_t off[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -507,16 +514,16 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             uint2 k[2], v[2];  // codes of the quarter, in writing order (zeros: not there)
             uint32_t ks, vs;   // its two scales
         };
-        auto fetch = [&](uint32_t t, Row (&R)[DP_ENT], uint32_t& missing) {
+        auto fetch = [&](uint32_t t, Row (&R)[ENT], uint32_t& missing) {
             missing = 0;
             const int32_t* pages = a.cache.page_table + (int64_t)w.b * a.cache.max_pages_per_seq;
             const int pos0 = (int)(t - w.t0) * DP_KEYS + e0;
 #pragma unroll
-            for (int i = 0; i < DP_ENT; ++i) {
-                const int pos = pos0 + DP_STEP * i;
+            for (int i = 0; i < ENT; ++i) {
+                const int pos = pos0 + STEP * i;
                 R[i].k[0] = R[i].k[1] = R[i].v[0] = R[i].v[1] = make_uint2(0, 0);
                 R[i].ks = R[i].vs = 0;
-                if (pos < w.s.len) {
+                if (mine(i) && pos < w.s.len) {
                     const int32_t pg = __ldg(pages + (pos >> a.page_shift));
                     if (pg >= 0 && pg < a.cache.n_phys_pages) {
                         const int slot = (pg << a.page_shift) | (pos & ((1 << a.page_shift) - 1));
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             }
         };
         uint32_t n = 0;  // tiles so far
-        Row R[DP_ENT];
+        Row R[ENT];
         uint32_t missing, t = lo, end;
         bool some = w.tiles(a, t, hi, end);
         if (some) fetch(t, R, missing);
@@ -558,10 +565,10 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             auto nan_pair = [](uint32_t x) { return ((x & 0x7f7fu) + 0x0101u) & 0x8080u; };
             uint32_t nan = 0;
 #pragma unroll
-            for (int i = 0; i < DP_ENT; ++i) nan |= nan_pair(R[i].vs);
+            for (int i = 0; i < ENT; ++i) nan |= nan_pair(R[i].vs);
             if (__any_sync(0xffffffffu, nan)) {
 #pragma unroll
-                for (int i = 0; i < DP_ENT; ++i) {
+                for (int i = 0; i < ENT; ++i) {
                     uint32_t x = nan_pair(R[i].vs);
                     R[i].vs &= ~(x | (x - (x >> 7)));  // 0x80 of a byte -> 0xff
                     x |= __shfl_xor_sync(0xffffffffu, x, 1);
@@ -572,23 +579,24 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             if (n >= 2) wait(&kempty[s], ((n >> 1) - 1) & 1u);
             uint8_t* kt = smem + DP_OFF_K + (size_t)s * DP_TILE;
 #pragma unroll
-            for (int i = 0; i < DP_ENT; ++i) store(kt + DP_STEP * 128 * i, R[i].k, R[i].ks);
+            for (int i = 0; i < ENT; ++i)
+                if (mine(i)) store(kt + STEP * 128 * i, R[i].k, R[i].ks);
             // which entries are there, one bit each (lane 4 x: entry x of the warp's eight)
 #pragma unroll
-            for (int i = 0; i < DP_ENT; ++i) {
+            for (int i = 0; i < ENT; ++i) {
                 uint32_t m = __ballot_sync(0xffffffffu, !((missing >> i) & 1u)) & 0x11111111u;
                 m = (m | m >> 3) & 0x03030303u;
                 m = (m | m >> 6) & 0x000f000fu;
                 m = (m | m >> 12) & 0xffu;
-                if (lane == 0) smem[DP_OFF_OK + (n & 3u) * 16 + DP_STEP / 8 * i + cw] = (uint8_t)m;
+                if (lane == 0 && mine(i)) smem[DP_OFF_OK + (n & 3u) * 16 + STEP / 8 * i + cw] = (uint8_t)m;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&kfull[s]);
-            uint2 vcode[DP_ENT][2];
-            uint32_t vscale[DP_ENT];
+            uint2 vcode[ENT][2];
+            uint32_t vscale[ENT];
 #pragma unroll
-            for (int i = 0; i < DP_ENT; ++i) {
+            for (int i = 0; i < ENT; ++i) {
                 vcode[i][0] = R[i].v[0];
                 vcode[i][1] = R[i].v[1];
                 vscale[i] = R[i].vs;
@@ -599,7 +607,8 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
             if (n >= 2) wait(&vempty[s], ((n >> 1) - 1) & 1u);
             uint8_t* vt = smem + DP_OFF_V + (size_t)s * DP_TILE;
 #pragma unroll
-            for (int i = 0; i < DP_ENT; ++i) store(vt + DP_STEP * 128 * i, vcode[i], vscale[i]);
+            for (int i = 0; i < ENT; ++i)
+                if (mine(i)) store(vt + STEP * 128 * i, vcode[i], vscale[i]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&vfull[s]);
@@ -904,7 +913,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1) dense_prefill_kernel(const Pref
     }
     tc_fence_before();
     __syncthreads();  // every accumulator has been read
-    if (wid == DP_W_MMA) {
+    if (wid == W_MMA) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
@@ -1010,12 +1019,12 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     // places there can be: units times the longest sequence's tiles and the weight
     const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS + DP_WEIGHT);
     const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);
-    LaunchCfg c(dim3(ctas), dim3(DP_THREADS), DP_SMEM, stream);
-    // By the average tokens of a sequence (cu_q is on the device): at most one row
+        // By the average tokens of a sequence (cu_q is on the device): at most one row
     // tile's take the paired kernel.  Measured, paired / not: 8 x 5 tokens over 65,536
-    // entries 72 / 81 us, 8 x 5 over 32,768 46 / 49, 200 x 5 over 400 to 4,000 60 / 63;
+    // entries 69 / 81 us, 8 x 5 over 32,768 46 / 49, 200 x 5 over 400 to 4,000 60 / 63;
     // 4096 tokens over 16,384 entries 497 / 485 us.
     const bool paired = a.T <= DP_TOK / 2 * (int64_t)a.B;
+    LaunchCfg c(dim3(ctas), dim3((unsigned)dp_threads(paired)), DP_SMEM, stream);
     auto kernel = a.out_bf16 ? (paired ? dense_prefill_kernel<false, true> : dense_prefill_kernel<false, false>)
                              : (paired ? dense_prefill_kernel<true, true> : dense_prefill_kernel<true, false>);
     e = cudaLaunchKernelEx(&c.cfg, kernel, (const PrefillDenseArgs)d);
