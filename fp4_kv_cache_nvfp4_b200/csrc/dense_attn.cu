@@ -31,6 +31,12 @@ csa2_status dense_args(const csa2_layer_desc* desc, const csa2_kv_cache* cache, 
         return CSA2_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 256) || ws_bytes < csa2_dense_attn_workspace_bytes(desc, B, prefill))
         return CSA2_ERR_WORKSPACE;
+    {
+        // a CTA stores rows while another may still read its queries
+        const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
+        const uint64_t n = (uint64_t)rows * kH * kD;
+        if (q0 < o0 + n * (out_dtype == CSA2_SRC_F32 ? 4 : 2) && o0 < q0 + n * 2) return CSA2_ERR_INVALID_ARG;
+    }
     for (const void* p : {(const void*)cache->codes, (const void*)cache->scales}) {
         cudaPointerAttributes at{};
         if (cudaPointerGetAttributes(&at, p) != cudaSuccess) return from_cuda(cudaErrorInvalidValue);

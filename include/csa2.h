@@ -369,9 +369,9 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
  * sequences' results, or, where they would be more work than T rows can be,
  * none does), a missing page (CSA2_DEV_PAGE; its entries count as not
  * seen).  Results do not vary from run to run.
- * q and out must be 16-byte aligned, codes and scales in device memory
- * (UNSUPPORTED if they are in host memory: these calls read them whole), the
- * cache smaller than 2^31 slots, B <= 65536 and T <= 2^26 (UNSUPPORTED).
+ * q and out must be 16-byte aligned and may not overlap (INVALID_ARG), codes
+ * and scales in device memory (UNSUPPORTED if they are in host memory: these
+ * calls read them whole), the cache smaller than 2^31 slots, B <= 65536 and T <= 2^26 (UNSUPPORTED).
  * max_len bounds seq_lens (1 <= max_len <= max_pages_per_seq * page_size).
  * workspace: device memory of csa2_dense_attn_workspace_bytes() bytes, 256-byte
  * aligned; what it holds before a call does not matter.  Calls sharing one
@@ -400,7 +400,9 @@ CSA2_API csa2_status csa2_dense_attn_prefill(const csa2_layer_desc* desc, const 
  *   page_table  [n_seqs][max_pages_per_seq] int32, -1 where there is no page
  *               (rewritten by these calls; the caches' own page_table is not read)
  *   refs        [n_phys_pages] int32, 16-byte aligned: how many entries of the
- *               page table hold the page; 0: free
+ *               page table hold the page; 0: free.  Whoever gives a row a page
+ *               besides these calls counts it (a page held but not counted can
+ *               be handed out again)
  *   seq_lens    [n_seqs] int32 entries; 0: the row is free
  * The counts are the allocator: a new page is the free one with the lowest
  * number.  Results do not vary from run to run.

@@ -56,6 +56,14 @@ def test_refusals(csa2, prefill):
         assert call(T=(1 << 26) + 1) == 2
 
 
+@pytest.mark.parametrize("prefill", [False, True])
+def test_results_over_queries_are_refused(csa2, prefill):
+    q, n = 0x100000, (5 if prefill else 2) * 16 * 128
+    for dt, size in ((csa2.F32, 4), (csa2.BF16, 2)):
+        for out in (q, q + 16, q + n * 2 - 16, q - n * size + 16):  # the last two share 16 bytes
+            assert _call(csa2, prefill, q=q, out=out, dt=dt, ws=0x1000000) == 1
+
+
 def test_workspace(csa2):
     d = csa2.default_desc(csa2.FULL, 1)
     for prefill in (False, True):
