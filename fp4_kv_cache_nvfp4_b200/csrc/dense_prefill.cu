@@ -731,6 +731,7 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
                             const float fa = fmaxf(f, 0x1p-20f), fb = f / fa;
                             const uint32_t ha = f2_to_h2(fa, fa), hb = f2_to_h2(fb, fb);
                             if (x == 1) {
+                                tmem_wait_st();  // the earlier columns' P, stored above, is read back
 #pragma unroll 1
                                 for (int y = 0; y < 64; y += 16) {
                                     uint32_t p[16];
