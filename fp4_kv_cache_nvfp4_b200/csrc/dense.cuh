@@ -53,13 +53,22 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t b2) {
     return d;
 }
 
-// fp16 pair of what the fp16 pair `h` leaves of (lo, hi): together 22 bits
-__device__ __forceinline__ uint32_t rest_h2(float lo, float hi, uint32_t h) {
+// fp32 results carry each weight as two fp16 terms, hi + lo * 2^-12, and multiply lo by V * 2^-12.
+// V is a multiple of 2^-10, so V * 2^-12 is exact in fp16; a weight is at most 2^15 and
+// leaves at most 2^3, so lo does not overflow.  The two terms hold 22 bits of every weight
+// from 2^-14 on, which is 2^-20 of the largest or less (that one is held as 2^6 or more);
+// smaller ones are rounded by up to 2^-37, 2^-43 of the largest.  (lo without the factor
+// would round by 2^-31 of the largest: a million small weights could lose 2^-11 of the sum.)
+constexpr float kLoScale = 4096.f;
+__device__ __forceinline__ float h2_lo(uint32_t h) {
     __half_raw r;
     r.x = (unsigned short)h;
-    const float a = lo - __half2float(__half(r));
-    r.x = (unsigned short)(h >> 16);
-    return f2_to_h2(a, hi - __half2float(__half(r)));
+    return __half2float(__half(r));
+}
+__device__ __forceinline__ float h2_hi(uint32_t h) { return h2_lo(h >> 16); }
+// lo of the pair (a, b) whose fp16 pair is `h`
+__device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t h) {
+    return f2_to_h2((a - h2_lo(h)) * kLoScale, (b - h2_hi(h)) * kLoScale);
 }
 
 // 8 dims of output row (token * 16 + head): o / l, and the lse by the thread of dim 0

@@ -446,7 +446,8 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                             }
                             if (SPLIT)
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) mma16816(O[8 * w + i], pl[u], x[0][i], x[1][i]);
+                                for (int i = 0; i < 8; ++i)  // V / kLoScale, exact
+                                    mma16816(O[8 * w + i], pl[u], hmul2(x[0][i], 0x0c000c00u), hmul2(x[1][i], 0x0c000c00u));
                         }
                     }
                 }

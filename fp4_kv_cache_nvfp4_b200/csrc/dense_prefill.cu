@@ -70,8 +70,8 @@ constexpr uint32_t kIdescPV = kIdescS | (1u << 16);  // B (V) has its dims conti
 // of an fp32 result's O grows with its tiles: relative error 2.7e-5 after 128 of
 // them.  After so many tiles of a row tile, O is added, with rounding, to sums in the
 // workspace (they stay in L2), and the products begin anew.  9 x 256 tokens over
-// 16,384 entries: 0.7e-6 and 567 us; after four tiles 1.2e-6 and 477 us, after one
-// 0.45e-6 and 729 us.
+// 16,384 entries (in a graph): 5.4e-7 and 627 us; after four tiles 1.1e-6 and 551 us,
+// after each 3.4e-7 and 755 us.
 constexpr uint32_t DP_DRAIN = 2;
 
 struct PrefillDenseArgs {
@@ -209,6 +209,14 @@ __device__ __forceinline__ void dp_mma_ts(uint32_t d, uint32_t ta, uint32_t b, u
         "r"(ta), "r"(b), "r"(kIdescPV), "r"(kDescHi), "r"(acc)
         : "memory");
 }
+// the same, D = D * 2^-12 + A . B (kLoScale)
+__device__ __forceinline__ void dp_mma_ts_lo_done(uint32_t d, uint32_t ta, uint32_t b) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.eq.b32 p, 0, 0;\n\tmov.b64 db, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p, 12;\n\t}" ::"r"(d),
+        "r"(ta), "r"(b), "r"(kIdescPV), "r"(kDescHi)
+        : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -247,6 +255,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
         "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
         "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+        "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr)
         : "memory");
 }
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
@@ -397,10 +415,16 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
         auto mma_pv = [&](int i, bool first) {  // O of row tile i += P . V tile in slot vs
             if (leader) {
                 const uint32_t v = vlo + vs * (DP_TILE >> 4), p = tmem + 128u * i, o = tmem + 256u + 128u * i;
+                if (SPLIT) {  // the low terms on kLoScale * O, then O = that / kLoScale + the high terms
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {  // P of 16 entries: 8 columns
-                    dp_mma_ts(o, p + 32u * (x >> 1) + 8u * (x & 1), v + 128u * x, x > 0 || !first);
-                    if (SPLIT) dp_mma_ts(o, p + 32u * (x >> 1) + 16u + 8u * (x & 1), v + 128u * x, 1);
+                    for (int x = 0; x < 8; ++x) dp_mma_ts(o, p + 32u * (x >> 1) + 16u + 8u * (x & 1), v + 128u * x, x > 0 || !first);
+                    dp_mma_ts_lo_done(o, p, v);
+#pragma unroll
+                    for (int x = 1; x < 8; ++x) dp_mma_ts(o, p + 32u * (x >> 1) + 8u * (x & 1), v + 128u * x, 1);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)  // P of 16 entries: 8 columns
+                        dp_mma_ts(o, p + 32u * (x >> 1) + 8u * (x & 1), v + 128u * x, x > 0 || !first);
                 }
             }
             __syncwarp();
@@ -689,6 +713,16 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
                         drained = true;
                         m_sum = m;
                         __syncwarp();
+                    } else if (SPLIT && t - first >= step) {  // the tile's low terms come on top of kLoScale * O
+#pragma unroll 1
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t v[32];
+                            tmem_ld32(tO + 32u * x, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kLoScale);
+                            tmem_st32(tO + 32u * x, v);
+                        }
                     }
                     const int nv = seen - (int)(t - w.t0) * DP_KEYS;  // entries of the tile this row sees
                     const uint4 ok = *reinterpret_cast<const uint4*>(smem + DP_OFF_OK + (n & 3u) * 16);
@@ -730,16 +764,27 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
                             // f as two fp16 factors: it may lie below fp16's range where P times f does not
                             const float fa = fmaxf(f, 0x1p-20f), fb = f / fa;
                             const uint32_t ha = f2_to_h2(fa, fa), hb = f2_to_h2(fb, fb);
+                            tmem_wait_st();  // what was stored above is read back: the earlier columns' P (and O)
                             if (x == 1) {
-                                tmem_wait_st();  // the earlier columns' P, stored above, is read back
 #pragma unroll 1
-                                for (int y = 0; y < 64; y += 16) {
-                                    uint32_t p[16];
+                                for (int y = 0; y < 64; y += SPLIT ? 32 : 16) {
+                                    uint32_t p[16], q[16];
                                     tmem_ld16(tS + y, p);
+                                    if (SPLIT) tmem_ld16(tS + y + 16, q);
                                     tmem_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) p[e] = hmul2(hmul2(p[e], ha), hb);
+                                    for (int e = 0; e < 16; ++e) {
+                                        if (SPLIT) {  // put together, rescaled and taken apart again
+                                            const float lo = (h2_lo(p[e]) + h2_lo(q[e]) * (1.f / kLoScale)) * f;
+                                            const float hi = (h2_hi(p[e]) + h2_hi(q[e]) * (1.f / kLoScale)) * f;
+                                            p[e] = f2_to_h2(lo, hi);
+                                            q[e] = rest_h2(lo, hi, p[e]);
+                                        } else {
+                                            p[e] = hmul2(hmul2(p[e], ha), hb);
+                                        }
+                                    }
                                     tmem_st16(tS + y, p);
+                                    if (SPLIT) tmem_st16(tS + y + 16, q);
                                 }
                             }
                             if (t - first >= step) {  // O is complete: S of this tile was issued after its last product

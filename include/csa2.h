@@ -340,9 +340,10 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
  *   out = sum_j exp(s_j - lse) v_j
  * There is no window branch: csa2_attn_lse_merge joins an fp32 result with
  * another one (a window's, another shard's).  Sums, maxima and partial
- * results are held in fp32; the weights exp(s_j - max) are rounded to fp16
- * (11 significant bits) for a bf16 result and carried as two fp16 terms (22
- * bits) for an fp32 result.
+ * results are held in fp32.  For a bf16 result the weights exp(s_j - max) are
+ * rounded to fp16 (11 significant bits; those below 2^-20 of the largest by up
+ * to 2^-31 of it), for an fp32 result they are carried as two fp16 terms (22
+ * bits; below 2^-20 of the largest 2^-43 of it).  lse sums them in fp32.
  *
  * Decode: one token per sequence, which sees entries [0, seq_lens[b]).
  *   q [B][16][128] bf16; out [B][16][128]; lse [B][16] fp32

@@ -35,3 +35,67 @@ def test_the_maximum_rises_inside_a_tile(csa2, n, dtype):
     out, lse, err = prefill(csa2, c, q, [0, n], DT[dtype], [L - n])
     assert err == 0
     check(out, lse, reference(q, c.rows(0), seen_of(L, n, L - n, 1)), f"{n} tokens, {dtype}")
+
+
+def sink_case(csa2, n, seed=11):
+    """n entries whose scores are all 0 and whose V is not negative, behind one entry
+    with V = 0 and a score of 6 q_0 16 / sqrt(128) for queries of q_0 in 16 channels."""
+    c = DenseCase(csa2, [n + 1], 64, seed=seed)
+    sl = c.slots(0, n + 1)
+    c.codes[sl, :64] = 0
+    c.codes[sl, 64:] &= 0x77
+    c.codes[sl[0], :8] = 0x77   # K = 6 in channels 0..15 ...
+    c.scales[sl[0], 0] = 0x38   # ... times 1
+    c.codes[sl[0], 64:] = 0
+    return c.upload()
+
+
+@pytest.mark.parametrize("kernel", ["decode", "draft", "prefill"])
+def test_fp32_results_keep_small_weights(csa2, kernel):
+    """One entry that takes nearly all the weight and has V = 0, 16 to 24 nats above
+    100,000 others that make up the result.  The largest weight is held as 2^6 or more, the
+    second fp16 term of a small one in steps of 2^-24 2^-12: a weight w of the largest is
+    rounded by w 2^-22, or 2^-37 / 2^6 = 2^-43 where that is more; scores by 128 2^-24 of sum |q k| / sqrt(128)
+    and 2^-22 of themselves, once above and once below the line; 2^x by 2^-20; and of
+    100,000 entries over 148 CTAs no sum is longer than 240 additions of 2^-24."""
+    n, tokens = 100_000, {"decode": 1, "draft": 5, "prefill": 33}[kernel]
+    c = sink_case(csa2, n)
+    nats = torch.linspace(16, 24, 16, dtype=torch.float64)
+    q = torch.zeros((tokens, 16, 128), dtype=torch.bfloat16)
+    q[:, :, :16] = (nats * 128 ** 0.5 / 96)[None, :, None].to(torch.bfloat16)
+    if kernel == "decode":
+        out, lse, err = decode(csa2, c, q, torch.float32)
+    else:
+        out, lse, err = prefill(csa2, c, q, [0, tokens], torch.float32)
+    assert err == 0
+    s = q[0, :, 0].double() * 96 / 128 ** 0.5
+    v = c.rows(0)[1:, 128:].sum(0)
+    want = v[None] / (torch.exp(s)[:, None] + n)
+    bound = 2.0 ** -43 * torch.exp(s) + 2.0 ** -22 + 2 * s * (128 * 2.0 ** -24 + 2.0 ** -22) + 2 * 2.0 ** -20 + 240 * 2.0 ** -24
+    for i in {0, tokens - 1}:
+        off = (out[i].double().cpu() - want).abs() / want
+        assert (off <= bound[:, None]).all(), f"token {i}: {(off.amax(1) / bound).tolist()} of the bound"
+        assert (lse[i].double().cpu() - torch.log(torch.exp(s) + n)).abs().max() <= bound.max()
+
+
+@pytest.mark.parametrize("half", [0, 1])
+def test_fp32_results_keep_small_weights_through_a_rise(csa2, half):
+    """The same with the entry that takes the weight last, in either half of the last
+    tile: what the earlier entries gave is rescaled, in O and in the tile itself."""
+    n = 128 + 64 * half + 20
+    c = sink_case(csa2, n)
+    c.table = c.table.clone()
+    sl = c.slots(0, n + 1)
+    for t in (c.codes, c.scales):
+        t[sl[-1]], t[sl[0]] = t[sl[0]].clone(), t[sl[-1]].clone()
+    c.upload()
+    nats = torch.linspace(16, 24, 16, dtype=torch.float64)
+    s = (nats * 128 ** 0.5 / 96).to(torch.bfloat16)
+    want = c.rows(0)[:-1, 128:].sum(0)[None] / (torch.exp(s.double() * 96 / 128 ** 0.5)[:, None] + n)
+    bound = 2.0 ** -43 * torch.exp(nats + 0.1) + 2.0 ** -21 + 2 * 25 * (128 * 2.0 ** -24 + 2.0 ** -22) + 2 * 2.0 ** -20 + n * 2.0 ** -24
+    for tokens in (1, 5, 20):
+        q = torch.zeros((tokens, 16, 128), dtype=torch.bfloat16)
+        q[:, :, :16] = s[None, :, None]
+        for out, _, err in [prefill(csa2, c, q, [0, tokens], torch.float32)] + ([decode(csa2, c, q, torch.float32)] if tokens == 1 else []):
+            off = (out.double().cpu() - want[None]).abs() / want
+            assert err == 0 and (off <= bound[None, :, None]).all(), f"{tokens}: {(off.amax(2) / bound).max()} of the bound"
