@@ -66,17 +66,19 @@ static_assert(DP_OFF_BAR % 8 == 0 && DP_SMEM <= 227 * 1024, "dense prefill layou
 constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 constexpr uint32_t kIdescPV = kIdescS | (1u << 16);  // B (V) has its dims contiguous
 
-// The tensor core's fp32 sums drop bits at every product, towards zero, so the bias
-// of an fp32 result's O grows with its tiles: relative error 2.7e-5 after 128 of
-// them.  After so many tiles of a row tile, O is added, with rounding, to sums in the
-// workspace (they stay in L2), and the products begin anew.  9 x 256 tokens over
-// 16,384 entries (in a graph): 5.4e-7 and 627 us; after four tiles 1.1e-6 and 551 us,
-// after each 3.4e-7 and 755 us.
-constexpr uint32_t DP_DRAIN = 2;
+// The tensor core's fp32 sums drop bits at every product, towards zero, so O's bias
+// grows with its tiles.  After so many tiles of a row tile, O is added, with rounding,
+// to sums in the workspace (they stay in L2), and the products begin anew.
+// fp32 results, 9 x 256 tokens over 16,384 entries (in a graph): every two tiles 5.4e-7
+// off and 627 us, every four 1.1e-6 and 551 us, every tile 3.4e-7 and 755 us, never 2.7e-5.
+// bf16 results: 64 tiles of 8 products lose 2^-15 at most, 1/128 of the result's own
+// step; without it 7.2e-4 were lost over 262,144 entries whose V have one sign, a sixth
+// of a step.  4096 tokens over 16,384 entries 485 us instead of 479.
+constexpr uint32_t dp_drain(bool split) { return split ? 2 : 64; }
 
 struct PrefillDenseArgs {
     DenseArgs a;
-    float4* sums;   // [ctas][2 row tiles][32 groups of 4 dims][128 rows] (fp32 results)
+    float4* sums;   // [ctas][2 row tiles][32 groups of 4 dims][128 rows]
     float* part_o;  // [2 * ctas][256 rows][128], times 2^(kPBias - m)
     float* part_m;  // [2 * ctas][256]
     float* part_l;  // [2 * ctas][256]
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
             __syncwarp();
         };
         // the k-th tile of a row tile (or group) begins O
-        auto fresh = [](uint32_t k) { return SPLIT ? k % DP_DRAIN == 0 : k == 0; };
+        auto fresh = [](uint32_t k) { return k % dp_drain(SPLIT) == 0; };
         auto commit = [&](uint64_t* bar) {
             if (leader) umma_commit(bar);
             __syncwarp();
@@ -688,147 +690,157 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
                     t += (uint32_t)i;
                     n += (uint32_t)i;
                 }
-                for (; t < end; t += step, n += step, ++sn) {
+                // O moves to the sums; it is complete, since S of the tile at t is and was issued after O's last product
+                auto move_out = [&]() {
+                    const float f = m_sum == -INFINITY ? 0.f : ex2(m_sum - m);
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t v[32];
+                        tmem_ld32(tO + 32u * x, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float4 u = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                                   __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+                            float4* at = sums + (8 * x + e) * 128;
+                            if (drained) {
+                                const float4 z = *at;
+                                u = make_float4(fmaf(z.x, f, u.x), fmaf(z.y, f, u.y), fmaf(z.z, f, u.z), fmaf(z.w, f, u.w));
+                            }
+                            *at = u;
+                        }
+                    }
+                    drained = true;
+                    m_sum = m;
+                    __syncwarp();
+                };
+                for (;;) {  // runs of tiles: an fp32 result moves O out inside them, a bf16 one between them
+                    const uint32_t stop = SPLIT ? end : min(end, t + step * dp_drain(SPLIT));
+                    for (; t < stop; t += step, n += step, ++sn) {
+                        wait(&sfull[i], sn & 1u);
+                        tc_fence_after();
+                        if (SPLIT && t - first >= step && ((t - first) / step) % dp_drain(SPLIT) == 0) move_out();
+                        else if (SPLIT && t - first >= step) {  // the tile's low terms come on top of kLoScale * O
+#pragma unroll 1
+                            for (int x = 0; x < 4; ++x) {
+                                uint32_t v[32];
+                                tmem_ld32(tO + 32u * x, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kLoScale);
+                                tmem_st32(tO + 32u * x, v);
+                            }
+                        }
+                        const int nv = seen - (int)(t - w.t0) * DP_KEYS;  // entries of the tile this row sees
+                        const uint4 ok = *reinterpret_cast<const uint4*>(smem + DP_OFF_OK + (n & 3u) * 16);
+                        const bool all = __all_sync(0xffffffffu, nv >= DP_KEYS && (ok.x & ok.y & ok.z & ok.w) == ~0u);
+                        // ---- 64 columns at a time: maximum, P over S, the sum ---------------------------------
+#pragma unroll 1
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t v[64];
+                            tmem_ld64(tS + 64u * x, v);
+                            tmem_wait_ld();
+                            if (!all) {  // the columns that this row sees, one bit each
+                                const int k = nv - 64 * x;
+                                uint64_t b = k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1ull;
+                                b &= x == 0 ? (uint64_t)ok.x | (uint64_t)ok.y << 32 : (uint64_t)ok.z | (uint64_t)ok.w << 32;
+#pragma unroll
+                                for (int e = 0; e < 64; ++e)
+                                    if (!((b >> e) & 1u)) v[e] = 0xff800000u;
+                            }
+                            float mx[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 4]));
+#pragma unroll
+                            for (int e = 8; e < 64; e += 8)
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    mx[y] = fmaxf(fmaxf(mx[y], __uint_as_float(v[e + y])), __uint_as_float(v[e + y + 4]));
+                            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // log2 domain
+                            const bool rise = top > -INFINITY && (m == -INFINITY || top + bias > kPMax);
+                            if (__any_sync(0xffffffffu, rise)) {
+                                // m takes whole numbers, so O, the sum and P of the tile's earlier columns are
+                                // rescaled by a power of two, exactly
+                                const float mn = ceilf(top), f = rise && m != -INFINITY ? ex2(m - mn) : 1.f;
+                                if (rise) {
+                                    m = mn;
+                                    bias = kPBias - mn;
+                                    l *= f;
+                                }
+                                __syncwarp();
+                                // f as two fp16 factors: it may lie below fp16's range where P times f does not
+                                const float fa = fmaxf(f, 0x1p-20f), fb = f / fa;
+                                const uint32_t ha = f2_to_h2(fa, fa), hb = f2_to_h2(fb, fb);
+                                tmem_wait_st();  // what was stored above is read back: the earlier columns' P (and O)
+                                if (x == 1) {
+#pragma unroll 1
+                                    for (int y = 0; y < 64; y += SPLIT ? 32 : 16) {
+                                        uint32_t p[16], q[16];
+                                        tmem_ld16(tS + y, p);
+                                        if (SPLIT) tmem_ld16(tS + y + 16, q);
+                                        tmem_wait_ld();
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) {
+                                            if (SPLIT) {  // put together, rescaled and taken apart again
+                                                const float lo = (h2_lo(p[e]) + h2_lo(q[e]) * (1.f / kLoScale)) * f;
+                                                const float hi = (h2_hi(p[e]) + h2_hi(q[e]) * (1.f / kLoScale)) * f;
+                                                p[e] = f2_to_h2(lo, hi);
+                                                q[e] = rest_h2(lo, hi, p[e]);
+                                            } else {
+                                                p[e] = hmul2(hmul2(p[e], ha), hb);
+                                            }
+                                        }
+                                        tmem_st16(tS + y, p);
+                                        if (SPLIT) tmem_st16(tS + y + 16, q);
+                                    }
+                                }
+                                if (t - first >= step) {  // O is complete: S of this tile was issued after its last product
+#pragma unroll 1
+                                    for (int y = 0; y < 128; y += 16) {
+                                        uint32_t o[16];
+                                        tmem_ld16(tO + y, o);
+                                        tmem_wait_ld();
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                        tmem_st16(tO + y, o);
+                                    }
+                                }
+                                tmem_wait_st();
+                            }
+                            // two columns per packed operation
+                            const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(bias, bias);
+                            uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                uint32_t p[16], q[16];
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    float p0, p1;
+                                    unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[32 * g + e]), __uint_as_float(v[32 * g + e + 1])), cc, bb),
+                                                 p0, p1);
+                                    p0 = ex2(p0);
+                                    p1 = ex2(p1);
+                                    if (e & 2) s1 = add_f32x2(s1, pack_f32x2(p0, p1));
+                                    else s0 = add_f32x2(s0, pack_f32x2(p0, p1));
+                                    p[e >> 1] = f2_to_h2(p0, p1);
+                                    if (SPLIT) q[e >> 1] = rest_h2(p0, p1, p[e >> 1]);
+                                }
+                                tmem_st16(tS + 64u * x + 32u * g, p);
+                                if (SPLIT) tmem_st16(tS + 64u * x + 32u * g + 16u, q);
+                            }
+                            float l0, l1;
+                            unpack_f32x2(add_f32x2(s0, s1), l0, l1);
+                            l += l0 + l1;
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&pfull[i]);
+                    }
+                    if (SPLIT || t >= end) break;
                     wait(&sfull[i], sn & 1u);
                     tc_fence_after();
-                    if (SPLIT && t - first >= step && ((t - first) / step) % DP_DRAIN == 0) {  // (O is complete: see below)
-                        const float f = m_sum == -INFINITY ? 0.f : ex2(m_sum - m);
-#pragma unroll 1
-                        for (int x = 0; x < 4; ++x) {
-                            uint32_t v[32];
-                            tmem_ld32(tO + 32u * x, v);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float4 u = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                                       __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-                                float4* at = sums + (8 * x + e) * 128;
-                                if (drained) {
-                                    const float4 z = *at;
-                                    u = make_float4(fmaf(z.x, f, u.x), fmaf(z.y, f, u.y), fmaf(z.z, f, u.z), fmaf(z.w, f, u.w));
-                                }
-                                *at = u;
-                            }
-                        }
-                        drained = true;
-                        m_sum = m;
-                        __syncwarp();
-                    } else if (SPLIT && t - first >= step) {  // the tile's low terms come on top of kLoScale * O
-#pragma unroll 1
-                        for (int x = 0; x < 4; ++x) {
-                            uint32_t v[32];
-                            tmem_ld32(tO + 32u * x, v);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kLoScale);
-                            tmem_st32(tO + 32u * x, v);
-                        }
-                    }
-                    const int nv = seen - (int)(t - w.t0) * DP_KEYS;  // entries of the tile this row sees
-                    const uint4 ok = *reinterpret_cast<const uint4*>(smem + DP_OFF_OK + (n & 3u) * 16);
-                    const bool all = __all_sync(0xffffffffu, nv >= DP_KEYS && (ok.x & ok.y & ok.z & ok.w) == ~0u);
-                    // ---- 64 columns at a time: maximum, P over S, the sum ---------------------------------
-#pragma unroll 1
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t v[64];
-                        tmem_ld64(tS + 64u * x, v);
-                        tmem_wait_ld();
-                        if (!all) {  // the columns that this row sees, one bit each
-                            const int k = nv - 64 * x;
-                            uint64_t b = k >= 64 ? ~0ull : k <= 0 ? 0ull : (1ull << k) - 1ull;
-                            b &= x == 0 ? (uint64_t)ok.x | (uint64_t)ok.y << 32 : (uint64_t)ok.z | (uint64_t)ok.w << 32;
-#pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                if (!((b >> e) & 1u)) v[e] = 0xff800000u;
-                        }
-                        float mx[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 4]));
-#pragma unroll
-                        for (int e = 8; e < 64; e += 8)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                mx[y] = fmaxf(fmaxf(mx[y], __uint_as_float(v[e + y])), __uint_as_float(v[e + y + 4]));
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // log2 domain
-                        const bool rise = top > -INFINITY && (m == -INFINITY || top + bias > kPMax);
-                        if (__any_sync(0xffffffffu, rise)) {
-                            // m takes whole numbers, so O, the sum and P of the tile's earlier columns are
-                            // rescaled by a power of two, exactly
-                            const float mn = ceilf(top), f = rise && m != -INFINITY ? ex2(m - mn) : 1.f;
-                            if (rise) {
-                                m = mn;
-                                bias = kPBias - mn;
-                                l *= f;
-                            }
-                            __syncwarp();
-                            // f as two fp16 factors: it may lie below fp16's range where P times f does not
-                            const float fa = fmaxf(f, 0x1p-20f), fb = f / fa;
-                            const uint32_t ha = f2_to_h2(fa, fa), hb = f2_to_h2(fb, fb);
-                            tmem_wait_st();  // what was stored above is read back: the earlier columns' P (and O)
-                            if (x == 1) {
-#pragma unroll 1
-                                for (int y = 0; y < 64; y += SPLIT ? 32 : 16) {
-                                    uint32_t p[16], q[16];
-                                    tmem_ld16(tS + y, p);
-                                    if (SPLIT) tmem_ld16(tS + y + 16, q);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        if (SPLIT) {  // put together, rescaled and taken apart again
-                                            const float lo = (h2_lo(p[e]) + h2_lo(q[e]) * (1.f / kLoScale)) * f;
-                                            const float hi = (h2_hi(p[e]) + h2_hi(q[e]) * (1.f / kLoScale)) * f;
-                                            p[e] = f2_to_h2(lo, hi);
-                                            q[e] = rest_h2(lo, hi, p[e]);
-                                        } else {
-                                            p[e] = hmul2(hmul2(p[e], ha), hb);
-                                        }
-                                    }
-                                    tmem_st16(tS + y, p);
-                                    if (SPLIT) tmem_st16(tS + y + 16, q);
-                                }
-                            }
-                            if (t - first >= step) {  // O is complete: S of this tile was issued after its last product
-#pragma unroll 1
-                                for (int y = 0; y < 128; y += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld16(tO + y, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st16(tO + y, o);
-                                }
-                            }
-                            tmem_wait_st();
-                        }
-                        // two columns per packed operation
-                        const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(bias, bias);
-                        uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            uint32_t p[16], q[16];
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float p0, p1;
-                                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[32 * g + e]), __uint_as_float(v[32 * g + e + 1])), cc, bb),
-                                             p0, p1);
-                                p0 = ex2(p0);
-                                p1 = ex2(p1);
-                                if (e & 2) s1 = add_f32x2(s1, pack_f32x2(p0, p1));
-                                else s0 = add_f32x2(s0, pack_f32x2(p0, p1));
-                                p[e >> 1] = f2_to_h2(p0, p1);
-                                if (SPLIT) q[e >> 1] = rest_h2(p0, p1, p[e >> 1]);
-                            }
-                            tmem_st16(tS + 64u * x + 32u * g, p);
-                            if (SPLIT) tmem_st16(tS + 64u * x + 32u * g + 16u, q);
-                        }
-                        float l0, l1;
-                        unpack_f32x2(add_f32x2(s0, s1), l0, l1);
-                        l += l0 + l1;
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[i]);
+                    move_out();
                 }
                 t = end;
                 n = n_end;
@@ -849,7 +861,7 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
                 auto load_o = [&](int x, uint32_t (&v)[32]) {
                     tmem_ld32(tO + 32u * x, v);
                     tmem_wait_ld();
-                    if (SPLIT && drained) {
+                    if (drained) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const float4 z = sums[(8 * x + e) * 128];

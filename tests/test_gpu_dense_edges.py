@@ -3,7 +3,7 @@ against the definition in 64 bits."""
 import pytest
 import torch
 
-from _dense_util import DenseCase, check, queries, reference
+from _dense_util import E2M1, DenseCase, check, queries, reference
 from test_gpu_dense import DT, decode, prefill, seen_of
 
 pytestmark = pytest.mark.gpu
@@ -99,3 +99,45 @@ def test_fp32_results_keep_small_weights_through_a_rise(csa2, half):
         for out, _, err in [prefill(csa2, c, q, [0, tokens], torch.float32)] + ([decode(csa2, c, q, torch.float32)] if tokens == 1 else []):
             off = (out.double().cpu() - want[None]).abs() / want
             assert err == 0 and (off <= bound[None, :, None]).all(), f"{tokens}: {(off.amax(2) / bound).max()} of the bound"
+
+
+class Shared:
+    """L entries with V >= 0 that B sequences share page by page, and the definition
+    in 64 bits on the GPU."""
+
+    def __init__(self, csa2, B, L, page=64):
+        g = torch.Generator(device="cuda").manual_seed(B + L)
+        codes = torch.randint(0, 256, (L, 128), generator=g, device="cuda", dtype=torch.uint8)
+        codes[:, 64:] &= 0x77
+        scales = (torch.rand((L, 16), generator=g, device="cuda") * 0.5 + 0.1).to(torch.float8_e4m3fn)
+        table = torch.randperm(L // page, generator=g, device="cuda").int().expand(B, -1).contiguous()
+        self.cache = csa2.KVCache.from_tensors(codes, scales.view(torch.uint8), table, page)
+        self.lens, self.max_len = [L] * B, L
+        x = torch.stack([E2M1.cuda()[(codes & 15).int()], E2M1.cuda()[(codes >> 4).int()]], 2).view(L, 256)
+        self.rows = x * scales.double().repeat_interleave(16, 1)  # (the order of the entries does not matter)
+
+    def reference(self, q):
+        out = []
+        for x in q.cuda().double().split(8):
+            s = x.reshape(-1, 128) @ self.rows[:, :128].T / 128 ** 0.5
+            out.append((torch.softmax(s, 1) @ self.rows[:, 128:]).view(-1, 16, 128))
+        return torch.cat(out)
+
+
+@pytest.mark.parametrize("kernel,B,T,L,steps", [("prefill", 1, 2368, 1 << 18, 64 * 8), ("draft", 148, 1184, 1 << 18, 64 * 8)])
+def test_bf16_results_do_not_drift(csa2, kernel, B, T, L, steps):
+    """Work that leaves each CTA whole units of very many entries.  The tensor core's sums
+    drop up to 2^-23 of themselves at each product, always towards zero; a sum begins anew
+    after `steps` of them, in which it grows from nothing, so at most steps 2^-24 of a
+    result are lost.  The results' rounding is 2^-8 / sqrt(3) of each and has no sign: over
+    148 x 16 x 128 of them 5 standard deviations are 2.1e-5."""
+    c = Shared(csa2, B, L)
+    q = queries(T, seed=L)
+    if kernel == "decode":
+        out, _, err = decode(csa2, c, q, torch.bfloat16)
+    else:
+        out, _, err = prefill(csa2, c, q, [T * b // B for b in range(B + 1)], torch.bfloat16)
+    assert err == 0
+    pick = torch.arange(148) * (T // 148)
+    off = float((out[pick].double() / c.reference(q[pick])).mean()) - 1
+    assert abs(off) <= steps * 2.0 ** -24 + 2.1e-5, f"{off:.3g}"
