@@ -50,11 +50,14 @@ static_assert(DD_WEIGHT % DD_WARPS == 0, "whole turns");
 constexpr int DD_STAGES = 2;                     // chunks of a warp's ring
 constexpr int DD_CODES = DD_CHUNK * kCodeBytes;  // 8 KiB per stage
 constexpr int DD_SCALES = DD_CHUNK * kScales;    // 1 KiB
-// The tensor core's fp32 sums drop bits at every product, towards zero: an fp32
-// result's O moves to shared memory, where it is added with rounding, after so many
-// chunks (32 products of a tile).  Relative error at 1M entries 2.0e-6 without, 0.6e-6 with
-// (72 us instead of 66; after two chunks 0.4e-6, 79 us).
-constexpr uint32_t DD_DRAIN = 4;
+// The tensor core's fp32 sums drop bits at every product, towards zero: a warp's O
+// moves to shared memory, where it is added with rounding, after so many chunks.
+// fp32 results: four chunks of eight products, 0.6e-6 off at 1M entries instead of 2.0e-6
+// (72 us instead of 66; after two chunks 0.4e-6, 79 us).  bf16 results: 64 chunks of four
+// products lose 2^-16 at most; without it 3.4e-4 were lost where a CTA has 524,288 entries
+// whose V have one sign, a tenth of the result's own step (8 x 262,144 entries 85.4 us
+// instead of 84.6).
+constexpr uint32_t dd_drain(bool split) { return split ? 4 : 64; }
 constexpr int DD_OROW = kD + 4;                  // floats per row of the joining slab (bank spread)
 constexpr size_t DD_OFF_CODES = 0;               // [warps][stages]
 constexpr size_t DD_OFF_SCALES = DD_OFF_CODES + (size_t)DD_WARPS * DD_STAGES * DD_CODES;
@@ -275,182 +278,192 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                     }
             };
             auto ratio = [](float from, float to) { return from == -INFINITY ? 0.f : ex2(from - to); };
-            float d0 = -INFINITY, d1 = -INFINITY;  // the maxima that the slab's sums are over (fp32 results)
+            // O moves to the slab; wm holds the maxima that the slab's sums are over
             bool drained = false;
-            uint32_t held = 0;                     // chunks in O
+            auto move_out = [&]() {
+                to_slab(1.f, 1.f, drained, drained ? ratio(wm[warp * kH + g], m0) : 0.f, drained ? ratio(wm[warp * kH + g + 8], m1) : 0.f);
+                __syncwarp();
+                if (t4 == 0) wm[warp * kH + g] = m0, wm[warp * kH + g + 8] = m1;
+                __syncwarp();
+                drained = true;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
+            };
+            uint32_t held = 0;  // chunks in O (fp32 results)
 
-            for (; c < seg1; c += DD_WARPS, ++done) {
-                if (SPLIT && held++ == DD_DRAIN) {
-                    held = 1;
-                    to_slab(1.f, 1.f, drained, ratio(d0, m0), ratio(d1, m1));
-                    drained = true;
-                    d0 = m0, d1 = m1;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
-                }
-                const int st = (int)(done & 1u);
-                if (!mbar_wait(&full[st], (done >> 1) & 1u, kDenseWaitLimit)) {  // give up: no copy stays in flight
-                    if (issued > done + 1) mbar_wait(&full[st ^ 1], ((done + 1) >> 1) & 1u, kDenseWaitLimit);
-                    if (lane == 0) dev_error(a.err, CSA2_DEV_TIMEOUT);
-                    c = c_next = hi;
-                    break;
-                }
-                const uint8_t* codes = my_codes + (size_t)st * DD_CODES;
-                uint8_t* scales = my_scales + (size_t)st * DD_SCALES;
-                const uint32_t boxes = st ? boxes1 : boxes0;
-                const int left = n - (int)(c - t0) * DD_CHUNK;  // entries from the chunk's first on
-                // Entries that are not there (behind the last one, of a missing page) get scale
-                // 0, so K and V are 0; their scores are hidden below.
-                const bool partial = boxes != all_boxes || left < DD_CHUNK;
-                auto gone = [&](int e) { return e >= left || !((boxes >> (e >> box_shift)) & 1u); };
-                if (partial) {
-#pragma unroll
-                    for (int e = lane; e < DD_CHUNK; e += 32)
-                        if (gone(e)) *reinterpret_cast<uint4*>(scales + e * kScales) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();  // the next copy into the stage comes after these writes
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int u0 = 0; u0 < DD_CHUNK; u0 += DD_UNIT, codes += DD_UNIT * kCodeBytes, scales += DD_UNIT * kScales) {
-                    // ---- S = Q K^T, four groups of eight entries ---------------------------------
-                    float S[DD_J][4];
-                    {
-                        uint4 kc[DD_J];
-                        uint32_t kl[DD_J], kh[DD_J];
-#pragma unroll
-                        for (int j = 0; j < DD_J; ++j) {
-                            kc[j] = *reinterpret_cast<const uint4*>(codes + j * 8 * kCodeBytes + off_k);
-                            const uint32_t s2 = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(scales + j * 8 * kScales + off_ks));
-                            kl[j] = __byte_perm(s2, 0u, 0x1010);
-                            kh[j] = __byte_perm(s2, 0u, 0x3232);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t x[DD_J][4];
-#pragma unroll
-                            for (int j = 0; j < DD_J; ++j) {
-                                const uint32_t w = i == 0 ? kc[j].x : i == 1 ? kc[j].y : i == 2 ? kc[j].z : kc[j].w;
-                                e2m1x8_to_h2x4(w, x[j][0], x[j][1], x[j][2], x[j][3]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) x[j][e] = hmul2(x[j][e], i < 2 ? kl[j] : kh[j]);
-                            }
-                            // group by group, so that four products lie between two of one sum
-#pragma unroll
-                            for (int j = 0; j < DD_J; ++j) {
-                                if (i == 0) mma16816_zero(S[j], qa[0], x[j][0], x[j][1]);
-                                else mma16816(S[j], qa[2 * i], x[j][0], x[j][1]);
-                            }
-#pragma unroll
-                            for (int j = 0; j < DD_J; ++j) mma16816(S[j], qa[2 * i + 1], x[j][2], x[j][3]);
-                        }
+            for (;;) {  // runs of chunks: an fp32 result moves O out inside them, a bf16 one between them
+                const uint32_t stop = SPLIT ? seg1 : min(seg1, c + DD_WARPS * dd_drain(SPLIT));
+                for (; c < stop; c += DD_WARPS, ++done) {
+                    if (SPLIT && held++ == dd_drain(SPLIT)) {
+                        held = 1;
+                        move_out();
                     }
-                    uint2 vc[DD_J][2];
-                    uint32_t vs[DD_J];  // scales of entries va and vb
-#pragma unroll
-                    for (int j = 0; j < DD_J; ++j) {
-                        vc[j][0] = *reinterpret_cast<const uint2*>(codes + j * 8 * kCodeBytes + off_va);
-                        vc[j][1] = *reinterpret_cast<const uint2*>(codes + j * 8 * kCodeBytes + off_vb);
-                        vs[j] = (uint32_t)scales[j * 8 * kScales + off_vs] |
-                                ((uint32_t)scales[j * 8 * kScales + (off_vs ^ (4 * kScales))] << 8);
+                    const int st = (int)(done & 1u);
+                    if (!mbar_wait(&full[st], (done >> 1) & 1u, kDenseWaitLimit)) {  // give up: no copy stays in flight
+                        if (issued > done + 1) mbar_wait(&full[st ^ 1], ((done + 1) >> 1) & 1u, kDenseWaitLimit);
+                        if (lane == 0) dev_error(a.err, CSA2_DEV_TIMEOUT);
+                        c = c_next = hi;
+                        break;
                     }
-                    if (u0 + DD_UNIT == DD_CHUNK) {  // the stage is in registers: the chunk after next goes there
+                    const uint8_t* codes = my_codes + (size_t)st * DD_CODES;
+                    uint8_t* scales = my_scales + (size_t)st * DD_SCALES;
+                    const uint32_t boxes = st ? boxes1 : boxes0;
+                    const int left = n - (int)(c - t0) * DD_CHUNK;  // entries from the chunk's first on
+                    // Entries that are not there (behind the last one, of a missing page) get scale
+                    // 0, so K and V are 0; their scores are hidden below.
+                    const bool partial = boxes != all_boxes || left < DD_CHUNK;
+                    auto gone = [&](int e) { return e >= left || !((boxes >> (e >> box_shift)) & 1u); };
+                    if (partial) {
+#pragma unroll
+                        for (int e = lane; e < DD_CHUNK; e += 32)
+                            if (gone(e)) *reinterpret_cast<uint4*>(scales + e * kScales) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();  // the next copy into the stage comes after these writes
                         __syncwarp();
-                        if (c_next < hi) {
-                            const uint32_t x = issue(st);
-                            if (st) boxes1 = x;
-                            else boxes0 = x;
-                        }
                     }
-                    // ---- weights: log2 domain, minus the maximum plus kPBias ------------------------
 #pragma unroll
-                    for (int j = 0; j < DD_J; ++j) {
-                        S[j][0] = fmaf(S[j][0], c0, bias0);
-                        S[j][1] = fmaf(S[j][1], c0, bias0);
-                        S[j][2] = fmaf(S[j][2], c1, bias1);
-                        S[j][3] = fmaf(S[j][3], c1, bias1);
-                    }
-                    float mx0 = fmaxf(S[0][0], S[0][1]), mx1 = fmaxf(S[0][2], S[0][3]);
+                    for (int u0 = 0; u0 < DD_CHUNK; u0 += DD_UNIT, codes += DD_UNIT * kCodeBytes, scales += DD_UNIT * kScales) {
+                        // ---- S = Q K^T, four groups of eight entries ---------------------------------
+                        float S[DD_J][4];
+                        {
+                            uint4 kc[DD_J];
+                            uint32_t kl[DD_J], kh[DD_J];
 #pragma unroll
-                    for (int j = 1; j < DD_J; ++j) {
-                        mx0 = fmaxf(fmaxf(mx0, S[j][0]), S[j][1]);
-                        mx1 = fmaxf(fmaxf(mx1, S[j][2]), S[j][3]);
-                    }
-                    if (__any_sync(0xffffffffu, partial || fmaxf(mx0, mx1) > kPMax || fminf(m0, m1) == -INFINITY)) {
-                        mx0 = mx1 = -INFINITY;
-#pragma unroll
-                        for (int j = 0; j < DD_J; ++j) {
-                            if (partial && gone(u0 + 8 * j + va)) S[j][0] = S[j][2] = -INFINITY;
-                            if (partial && gone(u0 + 8 * j + vb)) S[j][1] = S[j][3] = -INFINITY;
-                            mx0 = fmaxf(mx0, fmaxf(S[j][0], S[j][1]));
-                            mx1 = fmaxf(mx1, fmaxf(S[j][2], S[j][3]));
-                        }
-                        mx0 = quad_max(mx0) - bias0;  // the scores' maxima
-                        mx1 = quad_max(mx1) - bias1;
-                        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-                        const float nb0 = n0 == -INFINITY ? kPBias : kPBias - n0, nb1 = n1 == -INFINITY ? kPBias : kPBias - n1;
-                        const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
-#pragma unroll
-                        for (int j = 0; j < DD_J; ++j) {
-                            S[j][0] += nb0 - bias0;
-                            S[j][1] += nb0 - bias0;
-                            S[j][2] += nb1 - bias1;
-                            S[j][3] += nb1 - bias1;
-                        }
-                        m0 = n0, m1 = n1, bias0 = nb0, bias1 = nb1;
-                        l0 *= f0, l1 *= f1;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            O[i][0] *= f0;
-                            O[i][1] *= f0;
-                            O[i][2] *= f1;
-                            O[i][3] *= f1;
-                        }
-                    }
-                    uint32_t pa[DD_J / 2][4], pl[DD_J / 2][4];
-#pragma unroll
-                    for (int j = 0; j < DD_J; ++j) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) S[j][e] = ex2(S[j][e]);
-                        l0 += S[j][0] + S[j][1];
-                        l1 += S[j][2] + S[j][3];
-                        uint32_t* p = &pa[j >> 1][2 * (j & 1)];
-                        p[0] = f2_to_h2(S[j][0], S[j][1]);
-                        p[1] = f2_to_h2(S[j][2], S[j][3]);
-                        if (SPLIT) {  // what the first fp16 term leaves
-                            pl[j >> 1][2 * (j & 1)] = rest_h2(S[j][0], S[j][1], p[0]);
-                            pl[j >> 1][2 * (j & 1) + 1] = rest_h2(S[j][2], S[j][3], p[1]);
-                        }
-                    }
-                    // ---- O += P V: tile 8 w + i of eight columns g is dims 16 g + 8 w + i ------------
-#pragma unroll
-                    for (int u = 0; u < DD_J / 2; ++u) {  // sixteen entries
-                        const uint32_t sc0 = e4m3x2_to_h2(vs[2 * u]), sc1 = e4m3x2_to_h2(vs[2 * u + 1]);
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            // nibble pairs (entry va, entry vb) of one dim in one byte: even dims, then odd dims
-                            uint32_t x[2][8];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint2 a2 = vc[2 * u + j][0], b2 = vc[2 * u + j][1];
-                                const uint32_t p = w ? a2.y : a2.x, q = w ? b2.y : b2.x;
-                                const uint32_t ev = (p & 0x0f0f0f0fu) | ((q << 4) & 0xf0f0f0f0u);
-                                const uint32_t od = ((p >> 4) & 0x0f0f0f0fu) | (q & 0xf0f0f0f0u);
-                                e2m1x8_to_h2x4(ev, x[j][0], x[j][2], x[j][4], x[j][6]);
-                                e2m1x8_to_h2x4(od, x[j][1], x[j][3], x[j][5], x[j][7]);
+                            for (int j = 0; j < DD_J; ++j) {
+                                kc[j] = *reinterpret_cast<const uint4*>(codes + j * 8 * kCodeBytes + off_k);
+                                const uint32_t s2 = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(scales + j * 8 * kScales + off_ks));
+                                kl[j] = __byte_perm(s2, 0u, 0x1010);
+                                kh[j] = __byte_perm(s2, 0u, 0x3232);
                             }
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                x[0][i] = hmul2(x[0][i], sc0);
-                                x[1][i] = hmul2(x[1][i], sc1);
-                                mma16816(O[8 * w + i], pa[u], x[0][i], x[1][i]);
-                            }
-                            if (SPLIT)
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t x[DD_J][4];
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)  // V / kLoScale, exact
-                                    mma16816(O[8 * w + i], pl[u], hmul2(x[0][i], 0x0c000c00u), hmul2(x[1][i], 0x0c000c00u));
+                                for (int j = 0; j < DD_J; ++j) {
+                                    const uint32_t w = i == 0 ? kc[j].x : i == 1 ? kc[j].y : i == 2 ? kc[j].z : kc[j].w;
+                                    e2m1x8_to_h2x4(w, x[j][0], x[j][1], x[j][2], x[j][3]);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) x[j][e] = hmul2(x[j][e], i < 2 ? kl[j] : kh[j]);
+                                }
+                                // group by group, so that four products lie between two of one sum
+#pragma unroll
+                                for (int j = 0; j < DD_J; ++j) {
+                                    if (i == 0) mma16816_zero(S[j], qa[0], x[j][0], x[j][1]);
+                                    else mma16816(S[j], qa[2 * i], x[j][0], x[j][1]);
+                                }
+#pragma unroll
+                                for (int j = 0; j < DD_J; ++j) mma16816(S[j], qa[2 * i + 1], x[j][2], x[j][3]);
+                            }
+                        }
+                        uint2 vc[DD_J][2];
+                        uint32_t vs[DD_J];  // scales of entries va and vb
+#pragma unroll
+                        for (int j = 0; j < DD_J; ++j) {
+                            vc[j][0] = *reinterpret_cast<const uint2*>(codes + j * 8 * kCodeBytes + off_va);
+                            vc[j][1] = *reinterpret_cast<const uint2*>(codes + j * 8 * kCodeBytes + off_vb);
+                            vs[j] = (uint32_t)scales[j * 8 * kScales + off_vs] |
+                                    ((uint32_t)scales[j * 8 * kScales + (off_vs ^ (4 * kScales))] << 8);
+                        }
+                        if (u0 + DD_UNIT == DD_CHUNK) {  // the stage is in registers: the chunk after next goes there
+                            __syncwarp();
+                            if (c_next < hi) {
+                                const uint32_t x = issue(st);
+                                if (st) boxes1 = x;
+                                else boxes0 = x;
+                            }
+                        }
+                        // ---- weights: log2 domain, minus the maximum plus kPBias ------------------------
+#pragma unroll
+                        for (int j = 0; j < DD_J; ++j) {
+                            S[j][0] = fmaf(S[j][0], c0, bias0);
+                            S[j][1] = fmaf(S[j][1], c0, bias0);
+                            S[j][2] = fmaf(S[j][2], c1, bias1);
+                            S[j][3] = fmaf(S[j][3], c1, bias1);
+                        }
+                        float mx0 = fmaxf(S[0][0], S[0][1]), mx1 = fmaxf(S[0][2], S[0][3]);
+#pragma unroll
+                        for (int j = 1; j < DD_J; ++j) {
+                            mx0 = fmaxf(fmaxf(mx0, S[j][0]), S[j][1]);
+                            mx1 = fmaxf(fmaxf(mx1, S[j][2]), S[j][3]);
+                        }
+                        if (__any_sync(0xffffffffu, partial || fmaxf(mx0, mx1) > kPMax || fminf(m0, m1) == -INFINITY)) {
+                            mx0 = mx1 = -INFINITY;
+#pragma unroll
+                            for (int j = 0; j < DD_J; ++j) {
+                                if (partial && gone(u0 + 8 * j + va)) S[j][0] = S[j][2] = -INFINITY;
+                                if (partial && gone(u0 + 8 * j + vb)) S[j][1] = S[j][3] = -INFINITY;
+                                mx0 = fmaxf(mx0, fmaxf(S[j][0], S[j][1]));
+                                mx1 = fmaxf(mx1, fmaxf(S[j][2], S[j][3]));
+                            }
+                            mx0 = quad_max(mx0) - bias0;  // the scores' maxima
+                            mx1 = quad_max(mx1) - bias1;
+                            const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+                            const float nb0 = n0 == -INFINITY ? kPBias : kPBias - n0, nb1 = n1 == -INFINITY ? kPBias : kPBias - n1;
+                            const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+#pragma unroll
+                            for (int j = 0; j < DD_J; ++j) {
+                                S[j][0] += nb0 - bias0;
+                                S[j][1] += nb0 - bias0;
+                                S[j][2] += nb1 - bias1;
+                                S[j][3] += nb1 - bias1;
+                            }
+                            m0 = n0, m1 = n1, bias0 = nb0, bias1 = nb1;
+                            l0 *= f0, l1 *= f1;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                O[i][0] *= f0;
+                                O[i][1] *= f0;
+                                O[i][2] *= f1;
+                                O[i][3] *= f1;
+                            }
+                        }
+                        uint32_t pa[DD_J / 2][4], pl[DD_J / 2][4];
+#pragma unroll
+                        for (int j = 0; j < DD_J; ++j) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) S[j][e] = ex2(S[j][e]);
+                            l0 += S[j][0] + S[j][1];
+                            l1 += S[j][2] + S[j][3];
+                            uint32_t* p = &pa[j >> 1][2 * (j & 1)];
+                            p[0] = f2_to_h2(S[j][0], S[j][1]);
+                            p[1] = f2_to_h2(S[j][2], S[j][3]);
+                            if (SPLIT) {  // what the first fp16 term leaves
+                                pl[j >> 1][2 * (j & 1)] = rest_h2(S[j][0], S[j][1], p[0]);
+                                pl[j >> 1][2 * (j & 1) + 1] = rest_h2(S[j][2], S[j][3], p[1]);
+                            }
+                        }
+                        // ---- O += P V: tile 8 w + i of eight columns g is dims 16 g + 8 w + i ------------
+#pragma unroll
+                        for (int u = 0; u < DD_J / 2; ++u) {  // sixteen entries
+                            const uint32_t sc0 = e4m3x2_to_h2(vs[2 * u]), sc1 = e4m3x2_to_h2(vs[2 * u + 1]);
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {
+                                // nibble pairs (entry va, entry vb) of one dim in one byte: even dims, then odd dims
+                                uint32_t x[2][8];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const uint2 a2 = vc[2 * u + j][0], b2 = vc[2 * u + j][1];
+                                    const uint32_t p = w ? a2.y : a2.x, q = w ? b2.y : b2.x;
+                                    const uint32_t ev = (p & 0x0f0f0f0fu) | ((q << 4) & 0xf0f0f0f0u);
+                                    const uint32_t od = ((p >> 4) & 0x0f0f0f0fu) | (q & 0xf0f0f0f0u);
+                                    e2m1x8_to_h2x4(ev, x[j][0], x[j][2], x[j][4], x[j][6]);
+                                    e2m1x8_to_h2x4(od, x[j][1], x[j][3], x[j][5], x[j][7]);
+                                }
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    x[0][i] = hmul2(x[0][i], sc0);
+                                    x[1][i] = hmul2(x[1][i], sc1);
+                                    mma16816(O[8 * w + i], pa[u], x[0][i], x[1][i]);
+                                }
+                                if (SPLIT)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)  // V / kLoScale, exact
+                                        mma16816(O[8 * w + i], pl[u], hmul2(x[0][i], 0x0c000c00u), hmul2(x[1][i], 0x0c000c00u));
+                            }
                         }
                     }
                 }
+                if (SPLIT || c >= seg1) break;
+                move_out();
             }
 
             // ---- join the warps' results of the segment ------------------------------
@@ -458,6 +471,8 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
             l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+            const float s0 = drained ? wm[warp * kH + g] : -INFINITY, s1 = drained ? wm[warp * kH + g + 8] : -INFINITY;
+            __syncwarp();
             if (t4 == 0) {
                 wm[warp * kH + g] = m0;
                 wm[warp * kH + g + 8] = m1;
@@ -471,7 +486,7 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                 M0 = fmaxf(M0, wm[w * kH + g]);
                 M1 = fmaxf(M1, wm[w * kH + g + 8]);
             }
-            to_slab(ratio(m0, M0), ratio(m1, M1), SPLIT && drained, ratio(d0, M0), ratio(d1, M1));
+            to_slab(ratio(m0, M0), ratio(m1, M1), drained, ratio(s0, M0), ratio(s1, M1));
             __syncthreads();
             if (tid < kH * 16) {
                 const int h = tid >> 4, d8 = (tid & 15) * 8;  // 16 heads x 16 threads of 8 dims

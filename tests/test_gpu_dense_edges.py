@@ -124,7 +124,8 @@ class Shared:
         return torch.cat(out)
 
 
-@pytest.mark.parametrize("kernel,B,T,L,steps", [("prefill", 1, 2368, 1 << 18, 64 * 8), ("draft", 148, 1184, 1 << 18, 64 * 8)])
+@pytest.mark.parametrize("kernel,B,T,L,steps", [
+    ("prefill", 1, 2368, 1 << 18, 64 * 8), ("draft", 148, 1184, 1 << 18, 64 * 8), ("decode", 148, 148, 1 << 19, 64 * 4)])
 def test_bf16_results_do_not_drift(csa2, kernel, B, T, L, steps):
     """Work that leaves each CTA whole units of very many entries.  The tensor core's sums
     drop up to 2^-23 of themselves at each product, always towards zero; a sum begins anew
