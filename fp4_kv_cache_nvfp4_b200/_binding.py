@@ -198,8 +198,8 @@ def swa_replay(h, w_kv, seq_lens, swa_kv, B: int, window: int = 128, err=None, s
 
 
 def test_set_wait_limit(polls: int) -> int:
-    """Test hook: poll limit of the block-level indexer's cp.async copy-ring
-    waits (returns the previous limit)."""
+    """Test hook: poll limit of the waits of the block-level indexer's cp.async
+    copy ring and of dense attention (returns the previous limit)."""
     return int(lib().csa2_test_set_wait_limit(polls))
 
 

@@ -54,6 +54,7 @@ csa2_status dense_args(const csa2_layer_desc* desc, const csa2_kv_cache* cache, 
     a.ratio = desc->ratio;
     a.page_shift = page_shift_of(*cache);
     a.out_bf16 = out_dtype == CSA2_SRC_BF16;
+    a.wait_limit = test_wait_limit();
     return CSA2_OK;
 }
 

@@ -299,9 +299,11 @@ __global__ void __launch_bounds__(DD_THREADS, 1)
                         move_out();
                     }
                     const int st = (int)(done & 1u);
-                    if (!mbar_wait(&full[st], (done >> 1) & 1u, kDenseWaitLimit)) {  // give up: no copy stays in flight
-                        if (issued > done + 1) mbar_wait(&full[st ^ 1], ((done + 1) >> 1) & 1u, kDenseWaitLimit);
+                    if (!mbar_wait(&full[st], (done >> 1) & 1u, a.wait_limit)) {
+                        // give up: report, then wait, again with a limit, for the warp's own copies (one or two)
                         if (lane == 0) dev_error(a.err, CSA2_DEV_TIMEOUT);
+                        mbar_wait(&full[st], (done >> 1) & 1u, kDenseWaitLimit);
+                        if (issued > done + 1) mbar_wait(&full[st ^ 1], ((done + 1) >> 1) & 1u, kDenseWaitLimit);
                         c = c_next = hi;
                         break;
                     }

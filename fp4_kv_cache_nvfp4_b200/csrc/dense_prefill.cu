@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
     // bounded; a thread that gave up once does not wait any more
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity, kDenseWaitLimit)) {
+        if (!dead && !mbar_wait(bar, parity, a.wait_limit)) {
             dead = true;
             *s_timeout = 1;
         }
@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
             }
         }
         commit(mma_done);
+        // whatever was given up above: the products in flight end before TMEM is freed
         if (!mbar_wait(mma_done, 0u, kDenseWaitLimit)) *s_timeout = 1;
     } else if (lo < hi && wid >= DP_W_CONV) {
         // ================= converters: FP4 rows -> fp16 operand tiles =================

@@ -202,9 +202,10 @@ constexpr size_t K2_OFF_BAR = align16(K2_OFF_NBLK + K2_MAX_SEQS * 4);  // full[3
 constexpr size_t K2_OFF_MISC = align16(K2_OFF_BAR + 2 * K2_STAGES * 8);  // w (float4), last, timeout
 constexpr size_t K2_SMEM = align16(K2_OFF_MISC + 32);
 constexpr uint32_t kWaitLimit = 1u << 22;
-// Poll limit of the block-scoring copy ring's waits (cp.async rows only): the
-// default above, lowered only by csa2_test_set_wait_limit.
+// Poll limit of the block-scoring copy ring's waits (cp.async rows only) and of
+// dense attention's: the default above, lowered only by csa2_test_set_wait_limit.
 static std::atomic<uint32_t> g_copy_wait_limit{kWaitLimit};
+uint32_t test_wait_limit() { return g_copy_wait_limit.load(std::memory_order_relaxed); }
 static_assert(K2_OFF_QD % 16 == 0 && K2_OFF_BAR % 8 == 0 && K2_OFF_MISC % 16 == 0, "K2 shared-memory layout");
 
 struct BlockArgs {
@@ -2251,7 +2252,7 @@ cudaError_t launch_block_topk(const csa2_kv_cache& cache, const uint16_t* q_idx,
     // leave bulk copies in flight into the CTA's shared memory when it exits.
     // The cp.async ring's producers drain their own copies before they leave,
     // so its limit may be lowered (csa2_test_set_wait_limit).
-    a.wait_limit = a.tma ? kWaitLimit : g_copy_wait_limit.load(std::memory_order_relaxed);
+    a.wait_limit = a.tma ? kWaitLimit : test_wait_limit();
     if (nblk > keep) {
         const int64_t tiles = (int64_t)n * ((nblk + K2_TILE - 1) / K2_TILE);
         const int grid = (int)std::min<int64_t>(tiles, sm_count());

@@ -125,6 +125,9 @@ struct StageArgs {
 };
 cudaError_t launch_stage_rows(const StageArgs& a, int B, cudaStream_t stream);
 
+// The poll limit set by csa2_test_set_wait_limit (indexer.cu).
+uint32_t test_wait_limit();
+
 // Dense attention over every entry of the main KV (checks: dense_attn.cu).
 struct DenseArgs {
     csa2_kv_cache cache;
@@ -137,6 +140,7 @@ struct DenseArgs {
     int32_t* err;
     int32_t B, T, max_len, ratio, page_shift;
     bool out_bf16;
+    uint32_t wait_limit;      // polls before a wait gives up
 };
 // One token per sequence (dense_decode.cu).
 size_t dense_decode_ws_bytes();

@@ -487,10 +487,10 @@ CSA2_API csa2_status csa2_indexer_topk_noalloc(const csa2_layer_desc* desc, cons
 /* ---------------------------------------------------------------------- */
 /* Test hook with no counterpart on the pages: the poll limit of the bounded
  * waits in the block-level indexer's cp.async copy ring (the hierarchical
- * indexer's pooled rows), which otherwise give up after 2^22 polls.  A wait
- * that gives up sets CSA2_DEV_TIMEOUT in err_word; the kernel still drains its
- * own copies, reaches every barrier and returns, and that call's results are
- * undefined.  Lowering the limit (0 = every wait gives up at once) lets a test
+ * indexer's pooled rows) and in dense attention, which otherwise give up after
+ * 2^22 polls.  A wait that gives up sets CSA2_DEV_TIMEOUT in err_word; the
+ * kernel still drains its own copies (and products), reaches every barrier and
+ * returns, and that call's results are undefined.  Lowering the limit (0 = every wait gives up at once) lets a test
  * drive that path; polls above 2^22 are clamped.  Process-wide, read when a
  * call is launched; returns the previous limit.  Not for production use. */
 CSA2_API uint32_t csa2_test_set_wait_limit(uint32_t polls);

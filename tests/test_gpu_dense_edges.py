@@ -7,6 +7,7 @@ from _dense_util import E2M1, DenseCase, check, queries, reference
 from test_gpu_dense import DT, decode, prefill, seen_of
 
 pytestmark = pytest.mark.gpu
+DEV_PAGE, DEV_TIMEOUT = 0x2, 0x10
 
 
 @pytest.fixture(scope="module")
@@ -142,3 +143,39 @@ def test_bf16_results_do_not_drift(csa2, kernel, B, T, L, steps):
     pick = torch.arange(148) * (T // 148)
     off = float((out[pick].double() / c.reference(q[pick])).mean()) - 1
     assert abs(off) <= steps * 2.0 ** -24 + 2.1e-5, f"{off:.3g}"
+
+
+def test_waits_that_run_out_are_reported(csa2):
+    """A limit of no polls: every wait of the decode, prefill and draft kernels gives up
+    at once.  The kernels still wait for their copies and products, return and report,
+    and the next call, on the same workspace, is right."""
+    lens = [5000, 300]
+    c = DenseCase(csa2, lens, 64, seed=5)
+    q, d = queries(40, seed=6).cuda(), csa2.default_desc(csa2.FULL, 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    sl = i32(lens)
+    ws = torch.empty(csa2.dense_attn_workspace_bytes(d, 2, True), dtype=torch.uint8, device="cuda")
+
+    def calls(dt):
+        for n in (1, 4, 20):
+            out, lse = torch.zeros((2 * n, 16, 128), dtype=dt, device="cuda"), torch.zeros((2 * n, 16), device="cuda")
+            err = i32([0])
+            if n == 1:
+                csa2.dense_attn_decode(d, c.cache, q[:2], sl, out, lse, c.max_len, ws, err=err)
+            else:
+                csa2.dense_attn_prefill(d, c.cache, q[:2 * n], i32([0, n, 2 * n]), sl, out, lse, c.max_len, ws, err=err)
+            torch.cuda.synchronize()
+            yield n, out, lse, int(err)
+
+    for dt in DT.values():
+        prev = csa2.test_set_wait_limit(0)
+        try:
+            flags = [f for *_, f in calls(dt)]
+        finally:
+            assert csa2.test_set_wait_limit(prev) == 0
+        assert flags == [DEV_TIMEOUT] * 3
+        for n, out, lse, err in calls(dt):
+            assert err == 0
+            for b in (0, 1):
+                r = slice(n * b, n * b + n)
+                check(out[r], lse[r], reference(q[r].cpu(), c.rows(b), [lens[b]] * n), f"{n} tokens, sequence {b}")
