@@ -114,10 +114,12 @@ __device__ __forceinline__ int seen_by(const DenseArgs& a, const SeqQ& s, int i)
     const int64_t v = (s.p0 + i + 1) >> (a.ratio - 1);
     return v < s.len ? (int)v : s.len;
 }
-// Tiles of unit k: those its last token sees, one at least (it writes the rows)
-__device__ __forceinline__ uint32_t unit_tiles(const DenseArgs& a, const SeqQ& s, int k) {
-    return max(1u, (uint32_t)(seen_by(a, s, min((k + 1) * DP_TOK, s.nq) - 1) + DP_KEYS - 1) / DP_KEYS);
+// Entries that unit k's last token sees, and the tiles they take, one at least (it writes the rows)
+__device__ __forceinline__ int unit_seen(const DenseArgs& a, const SeqQ& s, int k) {
+    return seen_by(a, s, min((k + 1) * DP_TOK, s.nq) - 1);
 }
+__device__ __forceinline__ uint32_t tiles_of(int seen) { return max(1u, (uint32_t)(seen + DP_KEYS - 1) / DP_KEYS); }
+__device__ __forceinline__ uint32_t unit_tiles(const DenseArgs& a, const SeqQ& s, int k) { return tiles_of(unit_seen(a, s, k)); }
 // Places in the list of the units before k: a unit takes one for each tile and
 // DP_WEIGHT for what it costs besides (its Q, its rows: as long as a tile or two,
 // which counts where the units are short).  With A = p0 + 16 + 127 r and D = 128 r, a
@@ -149,6 +151,7 @@ __device__ __forceinline__ uint64_t places_before(const DenseArgs& a, const SeqQ
 struct Walk {
     int b, k, nk;
     SeqQ s;
+    int seen;         // entries that some token of the unit sees
     uint32_t t0, te;  // the unit's tiles in the list; its other places follow
     __device__ __forceinline__ void start(const DenseArgs& a, const uint32_t* at) {
         b = (int)at[0];
@@ -156,7 +159,8 @@ struct Walk {
         t0 = at[2];
         s = seq_q(a, b, false);
         nk = s.units();
-        te = t0 + unit_tiles(a, s, k);
+        seen = unit_seen(a, s, k);
+        te = t0 + tiles_of(seen);
     }
     __device__ __forceinline__ void next(const DenseArgs& a) {
         t0 = te + DP_WEIGHT;
@@ -167,7 +171,8 @@ struct Walk {
                 nk = s.units();
             } while (nk == 0 && b + 1 < a.B);
         }
-        te = t0 + unit_tiles(a, s, k);
+        seen = unit_seen(a, s, k);
+        te = t0 + tiles_of(seen);
     }
     // The first tile at or behind place t, and the end of the CTA's tiles of its unit.
     // False: there is none before hi.
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(dp_threads(PAIRED), 1) dense_prefill_kernel(co
                 const int pos = pos0 + STEP * i;
                 R[i].k[0] = R[i].k[1] = R[i].v[0] = R[i].v[1] = make_uint2(0, 0);
                 R[i].ks = R[i].vs = 0;
-                if (mine(i) && pos < w.s.len) {
+                if (mine(i) && pos < w.seen) {  // (what no token of the unit sees stays unread, its page with it)
                     const int32_t pg = __ldg(pages + (pos >> a.page_shift));
                     if (pg >= 0 && pg < a.cache.n_phys_pages) {
                         const int slot = (pg << a.page_shift) | (pos & ((1 << a.page_shift) - 1));

@@ -179,3 +179,25 @@ def test_waits_that_run_out_are_reported(csa2):
             for b in (0, 1):
                 r = slice(n * b, n * b + n)
                 check(out[r], lse[r], reference(q[r].cpu(), c.rows(b), [lens[b]] * n), f"{n} tokens, sequence {b}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,ratio", [(5, 1), (10, 1), (40, 1), (40, 2)])
+def test_a_missing_page_counts_where_it_is_seen(csa2, n, ratio, dtype):
+    """Pages of 16: the one behind the last entry that any token sees may be missing,
+    in a tile that they do see; the one that holds that entry is reported."""
+    L, first = 250, 100 * ratio
+    last = (first + n) // ratio                 # entries seen by the last token
+    page = -(-last // 16)                       # the first that nobody sees
+    assert page * 16 < 128 < L or n == 40
+    q = queries(n, seed=n)
+    for gone, want in ((page, 0), (page - 1, DEV_PAGE)):
+        c = DenseCase(csa2, [L], 16, seed=n)
+        pages = c.table.clone()
+        c.table[0, gone] = -1
+        c.upload()
+        out, lse, err = prefill(csa2, c, q, [0, n], DT[dtype], [first], ratio)
+        assert err == want
+        c.table = pages
+        hidden = None if gone == page else list(range(gone * 16, gone * 16 + 16))
+        check(out, lse, reference(q, c.rows(0), seen_of(L, n, first, ratio), hidden), f"page {gone}")
