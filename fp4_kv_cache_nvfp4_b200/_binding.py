@@ -343,6 +343,15 @@ def _device(t) -> int:
     return torch.cuda.current_device()
 
 
+def _cache_on(cache: KVCache, dev: int) -> None:
+    """The page table is on GPU `dev` and the main KV on no other GPU (the library
+    refuses one in host memory)."""
+    for name, t in (("page_table", cache.page_table), ("codes", cache.codes), ("scales", cache.scales)):
+        at = t.get_device()
+        if at != dev and (at >= 0 or t is cache.page_table):
+            raise ValueError(f"cache: {name} on {t.device}, expected cuda:{dev}")
+
+
 def _dense_checks(cache: KVCache, q, seq_lens, out, lse, workspace, err, B: int) -> tuple[int, int]:
     dev, T = _device(q), q.shape[0]
     _on_gpu("q", q, _BITS16, (T, 16, 128), dev)
@@ -353,8 +362,7 @@ def _dense_checks(cache: KVCache, q, seq_lens, out, lse, workspace, err, B: int)
     _on_gpu("err", err, _I32T, (1,), dev, optional=True)
     if cache.page_table.shape[0] < B:
         raise ValueError(f"seq_lens: {B} sequences, the page table has {cache.page_table.shape[0]}")
-    if cache.page_table.get_device() != dev:
-        raise ValueError(f"cache: on {cache.page_table.device}, expected cuda:{dev}")
+    _cache_on(cache, dev)
     return _OUT[out.dtype], dev
 
 

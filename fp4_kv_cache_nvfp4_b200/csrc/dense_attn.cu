@@ -37,10 +37,14 @@ csa2_status dense_args(const csa2_layer_desc* desc, const csa2_kv_cache* cache, 
         const uint64_t n = (uint64_t)rows * kH * kD;
         if (q0 < o0 + n * (out_dtype == CSA2_SRC_F32 ? 4 : 2) && o0 < q0 + n * 2) return CSA2_ERR_INVALID_ARG;
     }
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return from_cuda(e);
     for (const void* p : {(const void*)cache->codes, (const void*)cache->scales}) {
         cudaPointerAttributes at{};
         if (cudaPointerGetAttributes(&at, p) != cudaSuccess) return from_cuda(cudaErrorInvalidValue);
         if (at.type == cudaMemoryTypeHost || at.type == cudaMemoryTypeUnregistered) return CSA2_ERR_UNSUPPORTED;
+        if (at.type == cudaMemoryTypeDevice && at.device != dev) return CSA2_ERR_INVALID_ARG;
     }
     a.cache = *cache;
     a.q = q;
