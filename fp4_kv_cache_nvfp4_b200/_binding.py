@@ -160,6 +160,18 @@ def _on_gpu(name: str, t, dtypes, shape, dev: int, optional: bool = False) -> No
     raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
 
 
+def _readable(cache: KVCache):
+    """The cache's struct, for a call whose kernels read its arrays: none of them may
+    be in host memory that is not pinned (a handle made by from_tensors can be)."""
+    if not cache._seen_readable:
+        for name in ("page_table", "codes", "scales", "idx_k", "pooled"):
+            t = getattr(cache, name)
+            if t is not None and not t.is_cuda and not t.is_pinned():
+                raise ValueError(f"cache: {name} on {t.device}, which kernels cannot read")
+        cache._seen_readable = True
+    return ctypes.byref(cache._s)
+
+
 def abi_version() -> int:
     return int(lib().csa2_abi_version())
 
@@ -172,7 +184,7 @@ def device_accessible(t) -> int:
 def indexer_score_ids(desc: LayerDesc, cache: KVCache, level: int, q_idx, w, seq_lens, ids, id_offset: int,
                       scores, ids_out, n: int, max_len: int, err=None, stream=None) -> None:
     """Scores of the given ids (exact chains) and the ids plus id_offset."""
-    _check(lib().csa2_indexer_score_ids(ctypes.byref(desc), ctypes.byref(cache.struct()), level, _ptr(q_idx),
+    _check(lib().csa2_indexer_score_ids(ctypes.byref(desc), _readable(cache), level, _ptr(q_idx),
                                         _ptr(w), _ptr(seq_lens), _ptr(ids), ids.shape[-1], id_offset, _ptr(scores),
                                         _ptr(ids_out), n, max_len, _ptr(err), _stream(stream)), "indexer_score_ids")
 
@@ -231,6 +243,8 @@ class KVCache:
     main_kv_on_host: keep codes and scales (the main KV) in pinned host memory
     that the device reads in place; the indexer K stays in device memory."""
 
+    _seen_readable = False  # _readable found every array in place
+
     def __init__(self, n_phys_pages: int, page_size: int, page_table: torch.Tensor, device="cuda",
                  pooled: bool = True, main_kv_on_host: bool = False):
         n = n_phys_pages * page_size
@@ -258,7 +272,8 @@ class KVCache:
         may be rewritten in place): codes [n_slots, 128] and scales [n_slots, 16]
         uint8, page_table int32 [n_seqs, max_pages], idx_k [n_slots, 64] and
         pooled [n_slots / 8, 64] 16-bit.  Without idx_k and pooled the handle
-        serves the attention calls only."""
+        serves the attention and page calls and appends without an indexer K.
+        Arrays in host memory that is not pinned are refused by every call."""
         n = codes.shape[0]
         if page_size < 1 or n % page_size:
             raise ValueError(f"{n} slots are not whole pages of {page_size}")
@@ -295,7 +310,7 @@ def kv_quant_append(cache: KVCache, kv_src: torch.Tensor, idx_k_src, slot_mappin
                     err=None, stream=None) -> None:
     dt = BF16 if kv_src.dtype == torch.bfloat16 else F32
     n = slot_mapping.numel()
-    _check(lib().csa2_kv_quant_append(ctypes.byref(cache.struct()), _ptr(kv_src), dt, _ptr(idx_k_src), n, ratio,
+    _check(lib().csa2_kv_quant_append(_readable(cache), _ptr(kv_src), dt, _ptr(idx_k_src), n, ratio,
                                       _ptr(slot_mapping), _ptr(err), _stream(stream)), "kv_quant_append")
 
 
@@ -305,7 +320,7 @@ def workspace_bytes(desc: LayerDesc, level: int, n: int, max_len: int, prefill: 
 
 def indexer_topk(desc: LayerDesc, cache: KVCache, level: int, q_idx, w, seq_lens, out, n: int, max_len: int,
                  workspace: torch.Tensor, q_pos=None, cand_blocks=None, err=None, stream=None) -> None:
-    _check(lib().csa2_indexer_topk(ctypes.byref(desc), ctypes.byref(cache.struct()), level, _ptr(q_idx), _ptr(w),
+    _check(lib().csa2_indexer_topk(ctypes.byref(desc), _readable(cache), level, _ptr(q_idx), _ptr(w),
                                    _ptr(seq_lens), _ptr(q_pos), _ptr(cand_blocks), _ptr(out), None, n, max_len,
                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err),
                                    _stream(stream)), "indexer_topk")
@@ -313,14 +328,14 @@ def indexer_topk(desc: LayerDesc, cache: KVCache, level: int, q_idx, w, seq_lens
 
 def sparse_attn_decode(desc: LayerDesc, cache: KVCache, q, topk_idx, swa_kv, seq_lens, out, lse, B: int,
                        swa_lens=None, err=None, stream=None) -> None:
-    _check(lib().csa2_sparse_attn_decode(ctypes.byref(desc), ctypes.byref(cache.struct()), _ptr(q), _ptr(topk_idx),
+    _check(lib().csa2_sparse_attn_decode(ctypes.byref(desc), _readable(cache), _ptr(q), _ptr(topk_idx),
                                          _ptr(swa_kv), _ptr(seq_lens), _ptr(swa_lens), _ptr(out), _ptr(lse), B,
                                          _ptr(err), _stream(stream)), "sparse_attn_decode")
 
 
 def sparse_attn_prefill(desc: LayerDesc, cache: KVCache, q, topk_idx, q_pos, swa_kv, swa_start: int, seq_len: int,
                         out, lse, T: int, err=None, stream=None) -> None:
-    _check(lib().csa2_sparse_attn_prefill(ctypes.byref(desc), ctypes.byref(cache.struct()), _ptr(q), _ptr(topk_idx),
+    _check(lib().csa2_sparse_attn_prefill(ctypes.byref(desc), _readable(cache), _ptr(q), _ptr(topk_idx),
                                           _ptr(q_pos), _ptr(swa_kv), swa_start, seq_len, _ptr(out), _ptr(lse), T,
                                           _ptr(err), _stream(stream)), "sparse_attn_prefill")
 
@@ -484,7 +499,7 @@ def decode_layers(descs: list[LayerDesc], cache: KVCache, q_idx: list, w: list, 
     D = (LayerDesc * n)(*descs)
     arr = lambda xs: (ctypes.c_void_p * n)(*[_ptr(x) for x in xs])  # noqa: E731
     keep = [arr(q_idx), arr(w), arr(q), arr(swa_kv), arr(out), arr(lse)]
-    _check(lib().csa2_decode_layers(n, D, ctypes.byref(cache.struct()), ctypes.cast(keep[0], _P),
+    _check(lib().csa2_decode_layers(n, D, _readable(cache), ctypes.cast(keep[0], _P),
                                     ctypes.cast(keep[1], _P), ctypes.cast(keep[2], _P), ctypes.cast(keep[3], _P),
                                     _ptr(seq_lens), _ptr(swa_lens), _ptr(cand_blocks), _ptr(idx_sets),
                                     ctypes.cast(keep[4], _P), ctypes.cast(keep[5], _P), B, max_len,
@@ -496,6 +511,6 @@ def indexer_topk_noalloc(desc: LayerDesc, cache: KVCache, level: int, q_idx, w, 
                          cand_blocks=None, err=None, stream=None) -> None:
     """Decode indexer without a caller workspace (static 16 MiB library scratch);
     for callers that cannot allocate device memory at this point."""
-    _check(lib().csa2_indexer_topk_noalloc(ctypes.byref(desc), ctypes.byref(cache.struct()), level, _ptr(q_idx),
+    _check(lib().csa2_indexer_topk_noalloc(ctypes.byref(desc), _readable(cache), level, _ptr(q_idx),
                                            _ptr(w), _ptr(seq_lens), _ptr(cand_blocks), _ptr(out), n, max_len,
                                            _ptr(err), _stream(stream)), "indexer_topk_noalloc")
