@@ -32,10 +32,12 @@ csa2_status dense_args(const csa2_layer_desc* desc, const csa2_kv_cache* cache, 
     if (!ws || !aligned(ws, 256) || ws_bytes < csa2_dense_attn_workspace_bytes(desc, B, prefill))
         return CSA2_ERR_WORKSPACE;
     {
-        // a CTA stores rows while another may still read its queries
-        const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)out;
-        const uint64_t n = (uint64_t)rows * kH * kD;
-        if (q0 < o0 + n * (out_dtype == CSA2_SRC_F32 ? 4 : 2) && o0 < q0 + n * 2) return CSA2_ERR_INVALID_ARG;
+        // a CTA stores rows while another may still read its queries or store its own
+        const uintptr_t at[3] = {(uintptr_t)q, (uintptr_t)out, (uintptr_t)lse};
+        const uint64_t n = (uint64_t)rows * kH, size[3] = {n * kD * 2, n * kD * (out_dtype == CSA2_SRC_F32 ? 4 : 2), n * 4};
+        for (int i = 0; i < 3; ++i)
+            for (int j = 0; j < i; ++j)
+                if (at[i] < at[j] + size[j] && at[j] < at[i] + size[i]) return CSA2_ERR_INVALID_ARG;
     }
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);

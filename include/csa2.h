@@ -370,7 +370,7 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
  * sequences' results, or, where they would be more work than T rows can be,
  * none does), a missing page (CSA2_DEV_PAGE; its entries count as not
  * seen).  Results do not vary from run to run.
- * q and out must be 16-byte aligned and may not overlap (INVALID_ARG), codes
+ * q and out must be 16-byte aligned; q, out and lse may not overlap (INVALID_ARG), codes
  * and scales in the current device's memory (INVALID_ARG if they are on another
  * one, UNSUPPORTED if they are in host memory: these calls read them whole), the cache smaller than 2^31 slots, B <= 65536 and T <= 2^26 (UNSUPPORTED).
  * max_len bounds seq_lens (1 <= max_len <= max_pages_per_seq * page_size).
