@@ -366,10 +366,10 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
  * Detected on the device: a length outside [0, max_len] or a negative
  * q_start (CSA2_DEV_LEN; the sequence counts as empty), a range of cu_q that
  * is not ascending or not inside [0, T] (CSA2_DEV_LEN; that sequence's rows
- * stay as they were; if the other ranges then overlap, a row gets one of its
- * sequences' results, or, where they would be more work than T rows can be,
- * none does), a missing page (CSA2_DEV_PAGE; its entries count as not
- * seen).  Results do not vary from run to run.
+ * stay as they were; a row that several of the other ranges then hold is
+ * undefined, and where they would be more work than T rows can be, no row is
+ * written), a missing page (CSA2_DEV_PAGE; its entries count as not seen).
+ * Defined results do not vary from run to run.
  * q and out must be 16-byte aligned; q, out and lse may not overlap (INVALID_ARG), codes
  * and scales in the current device's memory (INVALID_ARG if they are on another
  * one, UNSUPPORTED if they are in host memory: these calls read them whole), the cache smaller than 2^31 slots, B <= 65536 and T <= 2^26 (UNSUPPORTED).
