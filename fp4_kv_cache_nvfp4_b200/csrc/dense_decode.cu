@@ -6,7 +6,7 @@
 // a sequence are joined by rescaling with 2^(m_part - m).  m follows the scores
 // lazily: it is raised only when a score exceeds it by more than 2^8, so O is
 // rescaled a few times per sequence.  p carries a factor of 2^7 (at most 2^15
-// as fp16), which keeps weights down to 2^-21 of the largest at fp16's full precision.
+// as fp16), which keeps weights down to 2^-20 of the largest at fp16's full precision.
 //
 // What bounds it.  144 bytes per entry for 8192 FLOP (16 heads share K and V):
 // HBM, if dequantisation and mma.sync stay behind the copies.  So
@@ -21,10 +21,11 @@
 //   * it dequantises 32 entries at a time in registers straight into mma.sync
 //     fragments (E2M1 x E4M3 is exact in fp16) and keeps its own m, l and O,
 //     joined once per sequence.  Nothing is written back to shared memory.
-// Measured: 8 x 262,144 entries 85 us (3.56 TB/s of K, V and scales, 203 TFLOP/s),
-// 1 x 1,048,573 with an fp32 result 72 us, 64 sequences of 509 to 32,768 entries 33 us.
-// What bounds the long ones is the issue of instructions (dequantisation, products
-// and weights of 32 entries), not the copies.
+// Measured (in a graph; a call from Python adds 1 to 9 us): 8 x 262,144 entries 86 us
+// (3.5 TB/s of K, V and scales, 200 TFLOP/s), 1 x 1,048,573 with an fp32 result 75 us,
+// 64 sequences of 509 to 32,768 entries 34 us.
+// What bounds the long ones is latency: two warps per scheduler (238 registers a thread)
+// issue 41 % of the time, and no unit is full (tensor 32 %, ALU 32 %, HBM 38 %).
 #include <algorithm>
 
 #include "common.cuh"
@@ -43,8 +44,8 @@ constexpr uint32_t DD_MIN_SHARE = 4;             // places per CTA at least
 // A sequence takes a place in the list for each chunk and so many for what it costs
 // besides (its Q and the joining of the warps: about 4 us, in which a CTA scores a
 // dozen chunks).  A multiple of the warps, so that the next sequence's chunks fall to
-// the warps in turn.  64 ragged
-// sequences: 46 us without, 38 with 8 places, 34 with 16; 300 short ones 59, 38, 35.
+// the warps in turn.  64 ragged sequences: 46 us without, 38 with 8 places, 34 with 16;
+// 300 short ones 59, 38, 35.
 constexpr uint32_t DD_WEIGHT = 16;
 static_assert(DD_WEIGHT % DD_WARPS == 0, "whole turns");
 constexpr int DD_STAGES = 2;                     // chunks of a warp's ring

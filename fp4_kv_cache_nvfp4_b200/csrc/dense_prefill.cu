@@ -20,13 +20,16 @@
 //                   other's products run
 // TMEM: S of both row tiles (P over them), O of both: all 512 columns.
 //
-// What bounds it: per (row tile, entry tile) the products take 1024 cycles of the
-// tensor core, the 16,384 exponentials 1024 cycles of the special-function
-// units, and the products' operands with the dequantised tiles' writes about 1000
-// cycles of shared memory, so three units are near their limits at once.
-// Measured: the last 4096 of 32,768 tokens at ratio 2 (16,384 entries) 485 to 497 us,
-// 1040 to 1060 TFLOP/s of the products that the mask leaves; drafts of 8 x 5 tokens
-// over 65,536 entries 69 us.
+// What bounds it: latency.  Per (row tile, entry tile) the products take 1024 cycles of
+// the tensor core and the 16,384 exponentials 1024 cycles of the special-function units,
+// but a pair of row tiles takes 4,170 cycles, not 2,048: the chain S -> softmax -> P ->
+// products of a row tile is serial, and two row tiles fill TMEM.  Both units are busy
+// 47 % of the time, instructions issue 41 %.  At 128 registers a thread all four kernels
+// spill (220 to 290 bytes stored).
+// Measured (in a graph): the last 4096 of 32,768 tokens at ratio 2 (16,384 entries) 486
+// us, 1060 TFLOP/s of the products that the mask leaves; in a run of seconds the power cap
+// lowers the clock from 1965 to 1850 MHz, and a call takes 523 us.  Drafts of 8 x 5
+// tokens over 65,536 entries 69 us.
 #include <string.h>
 
 #include <algorithm>
@@ -1083,10 +1086,10 @@ cudaError_t launch_dense_prefill(const DenseArgs& a, char* ws, cudaStream_t stre
     // places there can be: units times the longest sequence's tiles and the weight
     const int64_t units = (int64_t)a.T / DP_TOK + a.B, most = units * ((a.max_len + DP_KEYS - 1) / DP_KEYS + DP_WEIGHT);
     const unsigned ctas = (unsigned)std::min<int64_t>(std::min(n_sm[dev], kDenseCtas), most);
-        // By the average tokens of a sequence (cu_q is on the device): at most one row
+    // By the average tokens of a sequence (cu_q is on the device): at most one row
     // tile's take the paired kernel.  Measured, paired / not: 8 x 5 tokens over 65,536
-    // entries 69 / 81 us, 8 x 5 over 32,768 46 / 49, 200 x 5 over 400 to 4,000 60 / 63;
-    // 4096 tokens over 16,384 entries 497 / 485 us.
+    // entries 69 / 78 us, 8 x 5 over 32,768 45 / 48, 200 x 5 over 400 to 4,000 57 / 62;
+    // 4096 tokens over 16,384 entries 534 / 486 us.
     const bool paired = a.T <= DP_TOK / 2 * (int64_t)a.B;
     LaunchCfg c(dim3(ctas), dim3((unsigned)dp_threads(paired)), DP_SMEM, stream);
     auto kernel = a.out_bf16 ? (paired ? dense_prefill_kernel<false, true> : dense_prefill_kernel<false, false>)

@@ -343,7 +343,9 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
  * results are held in fp32.  For a bf16 result the weights exp(s_j - max) are
  * rounded to fp16 (11 significant bits; those below 2^-20 of the largest by up
  * to 2^-31 of it), for an fp32 result they are carried as two fp16 terms (22
- * bits; below 2^-20 of the largest 2^-43 of it).  lse sums them in fp32.
+ * bits; below 2^-20 of the largest 2^-43 of it).  lse sums them in fp32.  The
+ * tensor cores sum towards zero: a score over eight products, O over at most
+ * 2^9 before it is added with rounding (2^-15 of a bf16 result at most).
  *
  * Decode: one token per sequence, which sees entries [0, seq_lens[b]).
  *   q [B][16][128] bf16; out [B][16][128]; lse [B][16] fp32
@@ -374,8 +376,8 @@ CSA2_API csa2_status csa2_attn_lse_merge(int32_t n_parts, const float* out_parts
  * and scales in the current device's memory (INVALID_ARG if they are on another
  * one, UNSUPPORTED if they are in host memory: these calls read them whole), the cache smaller than 2^31 slots, B <= 65536 and T <= 2^26 (UNSUPPORTED).
  * max_len bounds seq_lens (1 <= max_len <= max_pages_per_seq * page_size).
- * workspace: device memory of csa2_dense_attn_workspace_bytes() bytes, 256-byte
- * aligned; what it holds before a call does not matter.  Calls sharing one
+ * workspace: device memory of csa2_dense_attn_workspace_bytes() bytes (2.5 MB
+ * for decode, 59 MB for prefill, whatever B), 256-byte aligned; what it holds before a call does not matter.  Calls sharing one
  * workspace must not overlap on the GPU. */
 CSA2_API size_t csa2_dense_attn_workspace_bytes(const csa2_layer_desc* desc, int32_t B, int32_t prefill);
 CSA2_API csa2_status csa2_dense_attn_decode(const csa2_layer_desc* desc, const csa2_kv_cache* cache, const uint16_t* q,
